@@ -11,6 +11,7 @@ is needed.
 from __future__ import annotations
 
 import argparse
+import concurrent.futures
 import glob
 import os
 import subprocess
@@ -46,7 +47,7 @@ def _build_lib(lib: str, objdir: str, extra, force: bool, verbose: bool) -> str:
     headers = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
     hdr_time = _newest(headers) if headers else 0.0
-    objs = []
+    objs, cmds = [], []
     for src in sources:
         obj = os.path.join(objdir, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
@@ -56,7 +57,11 @@ def _build_lib(lib: str, objdir: str, extra, force: bool, verbose: bool) -> str:
         cmd = [NVCC, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        subprocess.run(cmd, check=True)
+        cmds.append(cmd)
+    # one nvcc per source, as many at a time as there are cores; the first failure is raised
+    with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+        for f in [pool.submit(subprocess.run, cmd, check=True) for cmd in cmds]:
+            f.result()
     if force or not os.path.exists(lib) or os.path.getmtime(lib) < _newest(objs):
         tmp = lib + f".tmp{os.getpid()}"
         subprocess.run([NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl",
