@@ -11,6 +11,10 @@
  *   attn_sparse_csr_tc  attn_sparse_csr in bf16 / fp16 on the tensor cores.
  *   attn_csr_plan    the pattern bookkeeping of attn_sparse_csr_tc, once per pattern, into a
  *                    caller-owned buffer that attn_sparse_csr_tc_planned then reads.
+ *   attn_fwd_sinks   attn_fwd through a sliding window of the newest keys and the first few keys.
+ *   attn_decode_paged  the same for one new token per sequence, over a paged key/value cache.
+ *   attn_cache_append, attn_cache_fork, attn_cache_reserve, attn_cache_copy, attn_cache_compact
+ *                    that cache: new tokens written into its pages, and the bookkeeping of the pages.
  *
  * Conventions shared by every call
  *   - All tensor pointers are DEVICE pointers owned by the caller. The library allocates no
@@ -60,10 +64,14 @@ typedef enum {
   ATTN_ERR_UNSUPPORTED = 2, /* valid request this library does not run (e.g. bf16, D=96) */
   ATTN_ERR_CUDA = 3,        /* a CUDA runtime call failed (launch, device query)        */
   ATTN_ERR_DATA = 4,        /* device-side: bad cumulative lengths or CSR indices       */
-  ATTN_ERR_TIMEOUT = 5      /* device-side: a pipeline wait exceeded its bound          */
+  ATTN_ERR_TIMEOUT = 5,     /* device-side: a pipeline wait exceeded its bound          */
+  ATTN_ERR_PAGES = 6        /* device-side: attn_cache_reserve found too few free pages */
 } attn_status;
 
 typedef enum { ATTN_BF16 = 0, ATTN_F32 = 1, ATTN_F16 = 2 } attn_dtype;
+
+/* window_tokens of attn_fwd_sinks and attn_decode_paged: a window of every key. */
+#define ATTN_WINDOW_ALL (INT64_C(1) << 30)
 
 typedef enum { ATTN_BHSD = 0, ATTN_TND = 1 } attn_layout;
 
@@ -319,10 +327,163 @@ ATTN_API int attn_merge(const void* prev_out, const float* prev_max, const float
                void* out, float* out_max, float* out_sum, void* stream);
 
 /*
+ * attn_fwd_sinks -- attn_fwd through a sliding window with sink tokens.
+ *
+ * Query row i of a sequence stands at position p = i + Skv - Sq (bottom-right aligned: the queries
+ * are the newest tokens, so a chunk of a prompt can run against the keys of the chunks before it)
+ * and sees the key at position j iff
+ *     j <= p  and  (j > p - window_tokens  or  j < sink_tokens):
+ * the window_tokens newest keys, its own among them, and the first sink_tokens keys of the
+ * sequence, which stay visible (streaming attention's sinks). A row at p < 0 sees no key.
+ * window_tokens >= 1 (ATTN_WINDOW_ALL or more: every key up to p, as ATTN_MASK_CAUSAL_BOTTOMRIGHT);
+ * sink_tokens >= 0. Key tiles between the sinks and a block's windows are neither read nor
+ * multiplied, so the cost grows with window_tokens + sink_tokens and not with Skv.
+ * Other arguments, layouts, statistics, limits and errors are those of attn_fwd.
+ * NaN or infinite values at keys that a row does not see do not reach the row's scores; in the
+ * values v they may (0 * NaN) reach rows whose key tiles (128 keys; 32 for ATTN_F32) hold them.
+ */
+ATTN_API int attn_fwd_sinks(const void* q, const void* k, const void* v,
+                            const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                            int B, int Sq, int Skv, int Nq, int Nkv, int D, float scale,
+                            int64_t window_tokens, int64_t sink_tokens, int dtype, int layout,
+                            void* out, float* softmax_max, float* softmax_sum, void* stream);
+
+/*
+ * Paged key/value caches -- the arguments that the calls below share.
+ *
+ * k_cache, v_cache  pools of num_pages pages of page_size positions, of `dtype`:
+ *                     layout = ATTN_TND   [num_pages, page_size, Nkv, D]
+ *                     layout = ATTN_BHSD  [num_pages, Nkv, page_size, D]
+ *                   Page x starts at x * page_stride elements (0: pages are dense, page_size *
+ *                   Nkv * D apart; the two may be halves of one tensor [num_pages, 2, ...]).
+ * page_table        int32 [B, max_pages]: entry [b, i] is the page of positions i * page_size ..
+ *                   (i + 1) * page_size - 1 of row (sequence) b, or -1 where it has none. Pages may be
+ *                   shared between rows. Every max_pages * page_size <= 2^30.
+ * seq_lens          int32 [B]: tokens of each row, 0 <= seq_lens[b] <= max_pages * page_size.
+ * ref_count         int32 [num_pages]: in how many places a page is held (table entries, and whatever
+ *                   the caller counts beside them); 0 = free. Below 2^17.
+ * All of these are device arrays. Their contents are checked on the device: what is out of range sets
+ * ATTN_ERR_DATA in the status word and is skipped as stated for each call; it is never dereferenced.
+ * Tables have at most 8192 rows and 2^29 entries in the calls that change them.
+ */
+
+/*
+ * attn_decode_paged -- attention of one new token per row over a paged cache.
+ *
+ *   q, out  [B, Nq, D] of `dtype`;  softmax_max, softmax_sum  float32 [B, Nq] (both may be NULL)
+ * The query of row b stands at position seq_lens[b] - 1 (its own key and value are in the cache:
+ * attn_cache_append) and sees the keys that attn_fwd_sinks's rule gives that position: with
+ * ATTN_WINDOW_ALL all seq_lens[b] of them. GQA, scale and statistics are attn_fwd's. A row of length 0
+ * gives out 0, max -inf, sum 0. Only visible positions are read: table entries between the sinks and
+ * the window may be -1 (their pages freed), and what lies in a page behind the last token, or in
+ * positions that are not seen, may hold anything, NaN included.
+ * ATTN_BF16 and ATTN_F16 with D = 64 or 128, 16-byte aligned q, caches and page_stride run on the
+ * tensor cores (products exact, sums in float32, probabilities kept to 16 bits or more); other head
+ * sizes up to 256, alignments and ATTN_F32 on the CUDA cores in float32. Nq / Nkv may be any integer.
+ * workspace  device memory of attn_decode_workspace_size bytes, 16-byte aligned, filled with zeros
+ *            once before its first use; every call leaves it ready for the next one, of any sizes that
+ *            it is large enough for. Calls that may overlap on the device (other streams, graphs
+ *            replayed side by side) need a workspace each.
+ * Data errors: a length outside its range makes the row one of length 0; a page outside
+ * [0, num_pages) that holds visible positions leaves those out.
+ */
+ATTN_API int attn_decode_workspace_size(int Nq, int Nkv, int D, int dtype, int64_t* bytes);
+ATTN_API int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* page_table, const int32_t* seq_lens, int B, int Nq, int Nkv,
+                               int D, int num_pages, int page_size, int max_pages, int64_t page_stride,
+                               float scale, int64_t window_tokens, int64_t sink_tokens, int dtype,
+                               int layout, void* workspace, int64_t workspace_bytes, void* out,
+                               float* softmax_max, float* softmax_sum, void* stream);
+
+/*
+ * attn_cache_append -- write the keys and values of new tokens into the cache.
+ *
+ *   k, v        [T, Nkv, D] of `dtype`, packed row after row
+ *   cu_seqlens  int32 [B], cumulative tokens of each row without a leading zero, ending at T; NULL:
+ *               one token per row (T = B)
+ *   seq_lens    the rows' lengths WITH the new tokens: the n tokens of row b go to positions
+ *               seq_lens[b] - n .. seq_lens[b] - 1
+ * The pages must be there and the row's own (attn_cache_reserve); positions of two rows that share a
+ * page would be written twice. No other position is touched.
+ * Data errors: cumulative lengths that decrease or do not end at T; a token whose position is outside
+ * the table or whose page is outside [0, num_pages) is skipped.
+ */
+ATTN_API int attn_cache_append(const void* k, const void* v, const int32_t* page_table,
+                               const int32_t* seq_lens, const int32_t* cu_seqlens, int T, int B, int Nkv,
+                               int D, int num_pages, int page_size, int max_pages, int64_t page_stride,
+                               int dtype, int layout, void* k_cache, void* v_cache, void* stream);
+
+/*
+ * attn_cache_fork -- rows take the pages of other rows: fork, reorder and free sequences.
+ *
+ *   page_table [rows_in, max_pages] is replaced by page_table_out [rows_out, max_pages], whose row r
+ *   is row src_rows[r] of page_table, or empty (-1) where src_rows[r] is negative; src_rows int32
+ *   [rows_out]. A row may be taken any number of times (its pages are then shared) or not at all (its
+ *   pages lose a holder; at 0 they are free). So a fork of row a into the empty row b is the identity
+ *   with src_rows[b] = a, beam search's reordering is its parents, and freeing is -1.
+ *   ref_count_out = ref_count - holders in page_table + holders in page_table_out.
+ *   seq_lens_out[r] = seq_lens[src_rows[r]], or 0 (both may be NULL).
+ * Each output may be its input (in place; page_table then needs rows_out = rows_in); no other overlap.
+ * Nothing is copied: pages that rows share are separated when one of them writes (attn_cache_reserve).
+ * Data errors: src_rows[r] >= rows_in gives an empty row; an entry >= num_pages becomes -1.
+ */
+ATTN_API int attn_cache_fork(const int32_t* page_table, const int32_t* src_rows, const int32_t* ref_count,
+                             const int32_t* seq_lens, int rows_in, int rows_out, int max_pages,
+                             int num_pages, int32_t* page_table_out, int32_t* ref_count_out,
+                             int32_t* seq_lens_out, void* stream);
+
+/*
+ * attn_cache_reserve -- pages of their own for the rows' next tokens.
+ *
+ *   seq_lens    the rows' lengths WITH the new tokens;  new_tokens int32 [B], NULL: one per row
+ * Afterwards every page that holds a position seq_lens[b] - new_tokens[b] .. seq_lens[b] - 1 is held by
+ * row b alone. Missing pages (-1) are taken from the free ones, lowest index first, in the order of rows
+ * and columns; shared pages (ref_count > 1) are replaced in the same way and lose a holder, except that
+ * where all holders of a page ask in one call the first of them keeps it. A replaced page that holds
+ * earlier tokens of its row has to be copied: copies int32 [B, 2] gets (source, destination) for each
+ * row, or (-1, -1), for attn_cache_copy (once per layer whose caches share the table).
+ * All or nothing: where fewer pages are free than needed, ATTN_ERR_PAGES is recorded; where a length,
+ * an entry or a count is out of range (a held page with count 0 among them), ATTN_ERR_DATA. page_table
+ * and ref_count are then as before, and copies is all -1.
+ */
+ATTN_API int attn_cache_reserve(int32_t* page_table, int32_t* ref_count, const int32_t* seq_lens,
+                                const int32_t* new_tokens, int B, int max_pages, int num_pages,
+                                int page_size, int32_t* copies, void* stream);
+
+/*
+ * attn_cache_compact -- plan the moves that bring all live pages to the front of the pool.
+ *
+ * With n pages of count > 0, the k-th live page at or above n moves to the k-th free page below n.
+ *   page_map   int32 [num_pages]: the new index of each page, -1 for a free one (for holders of pages
+ *              beside the table)
+ *   page_table_out, ref_count_out: the renamed table and counts; each may be its input (in place)
+ *   copies     int32 [num_pages / 2, 2]: (source, destination) of each move, then (-1, -1), for
+ *              attn_cache_copy; sources and destinations are disjoint
+ *   live_pages int32 [1]: n
+ * Data errors: an entry outside the pool, or of a page with count 0, becomes -1.
+ */
+ATTN_API int attn_cache_compact(const int32_t* page_table, const int32_t* ref_count, int rows,
+                                int max_pages, int num_pages, int32_t* page_table_out,
+                                int32_t* ref_count_out, int32_t* page_map, int32_t* copies,
+                                int32_t* live_pages, void* stream);
+
+/*
+ * attn_cache_copy -- copy whole pages within a cache.
+ *
+ *   copies  int32 [n_copies, 2], 8-byte aligned: page copies[x][0] of both caches goes to page
+ *           copies[x][1]; pairs of negative entries are skipped. No page may be the destination of two
+ *           pairs, or of one and the source of another.
+ *   page_elems = page_size * Nkv * D elements are copied; page_stride as above (0: page_elems).
+ * Data errors: a pair with an entry outside [0, num_pages) is skipped.
+ */
+ATTN_API int attn_cache_copy(const int32_t* copies, int n_copies, int num_pages, int64_t page_elems,
+                             int64_t page_stride, int dtype, void* k_cache, void* v_cache, void* stream);
+
+/*
  * attn_get_last_error -- read and clear the calling device's status word.
  * Enqueues on `stream` a one-thread kernel that exchanges the word for 0 in one atomic step,
  * copies the old value back and synchronises `stream`. *device_status is then the first
- * device-side error (ATTN_ERR_DATA or ATTN_ERR_TIMEOUT) recorded by any launch on the current
+ * device-side error (ATTN_ERR_DATA, ATTN_ERR_TIMEOUT or ATTN_ERR_PAGES) recorded by any launch on the current
  * device since the previous read, or ATTN_OK. The word is per device, shared by all streams:
  * every launch that finished before the exchange is covered, and an error that a launch still
  * running on another stream records later is kept for the next read (none is lost). Calls on

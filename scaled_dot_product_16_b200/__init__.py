@@ -2,7 +2,8 @@
 
 The operations (attn_fwd, attn_fwd_masked, attn_fwd_accumulate, attn_sparse_csr,
 attn_sparse_csr_tc, attn_csr_plan_size, attn_csr_plan, attn_sparse_csr_tc_planned, attn_merge,
-attn_get_last_error) are the C-ABI calls declared in
+attn_fwd_sinks, attn_decode_paged, attn_cache_append, attn_cache_fork, attn_cache_reserve,
+attn_cache_compact, attn_cache_copy, attn_get_last_error) are the C-ABI calls declared in
 ``include/attn.h``; the functions here carry the same names and only marshal arguments (tensor
 data pointers, sizes, the current CUDA stream) into them. Every step of the computation runs in the library's CUDA kernels.
 There is no CPU path: if ``libattn.so`` is missing the first call raises.
@@ -22,13 +23,17 @@ __all__ = [
     "ATTN_BF16", "ATTN_F32", "ATTN_F16", "ATTN_BHSD", "ATTN_TND", "ATTN_MASK_NONE",
     "ATTN_MASK_CAUSAL_TOPLEFT", "ATTN_MASK_CAUSAL_BOTTOMRIGHT", "ATTN_MASK_BAND", "lib_path",
     "load_library", "attn_fwd_masked", "attn_sparse_csr_tc", "attn_csr_plan_size", "attn_csr_plan",
-    "attn_sparse_csr_tc_planned", "attn_sparse_csr_tc_noalloc",
+    "attn_sparse_csr_tc_planned", "attn_sparse_csr_tc_noalloc", "attn_fwd_sinks",
+    "attn_decode_workspace_size", "attn_decode_paged", "attn_cache_append", "attn_cache_fork",
+    "attn_cache_reserve", "attn_cache_compact", "attn_cache_copy", "ATTN_WINDOW_ALL",
 ]
 
-ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_DATA, ATTN_ERR_TIMEOUT = range(6)
+(ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_DATA, ATTN_ERR_TIMEOUT,
+ ATTN_ERR_PAGES) = range(7)
 ATTN_BF16, ATTN_F32, ATTN_F16 = 0, 1, 2
 ATTN_BHSD, ATTN_TND = 0, 1
 ATTN_MASK_NONE, ATTN_MASK_CAUSAL_TOPLEFT, ATTN_MASK_CAUSAL_BOTTOMRIGHT, ATTN_MASK_BAND = 0, 1, 2, 3
+ATTN_WINDOW_ALL = 1 << 30  # window_tokens that keeps every key
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -78,6 +83,23 @@ def load_library():
         lib.attn_sparse_csr_tc_noalloc.restype = I
         lib.attn_merge.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, P, P, P, P, P]
         lib.attn_merge.restype = I
+        lib.attn_fwd_sinks.argtypes = [P, P, P, P, P, I, I, I, I, I, I, F, I64, I64, I, I, P, P, P, P]
+        lib.attn_fwd_sinks.restype = I
+        lib.attn_decode_workspace_size.argtypes = [I, I, I, I, ctypes.POINTER(I64)]
+        lib.attn_decode_workspace_size.restype = I
+        lib.attn_decode_paged.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I64, F, I64, I64, I, I, P, I64,
+                                          P, P, P, P]
+        lib.attn_decode_paged.restype = I
+        lib.attn_cache_append.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I64, I, I, P, P, P]
+        lib.attn_cache_append.restype = I
+        lib.attn_cache_fork.argtypes = [P, P, P, P, I, I, I, I, P, P, P, P]
+        lib.attn_cache_fork.restype = I
+        lib.attn_cache_reserve.argtypes = [P, P, P, P, I, I, I, I, P, P]
+        lib.attn_cache_reserve.restype = I
+        lib.attn_cache_compact.argtypes = [P, P, I, I, I, P, P, P, P, P, P]
+        lib.attn_cache_compact.restype = I
+        lib.attn_cache_copy.argtypes = [P, I, I, I64, I64, I, P, P, P]
+        lib.attn_cache_copy.restype = I
         lib.attn_get_last_error.argtypes = [P, ctypes.POINTER(I)]
         lib.attn_get_last_error.restype = I
         lib.attn_status_string.argtypes = [I]
@@ -328,6 +350,149 @@ def attn_merge(prev_out, prev_max, prev_sum, cur_out, cur_max, cur_sum, *, S: in
                           _ptr(actual_seq_qlen, "actual_seq_qlen", _n(B), "int64"),
                           _ptr(out, "out", no, et), _ptr(out_max, "out_max", ns, f),
                           _ptr(out_sum, "out_sum", ns, f), _stream(stream)), "attn_merge")
+
+
+def attn_fwd_sinks(q, k, v, *, cu_seqlens_q=None, cu_seqlens_kv=None, B: int, Sq: int, Skv: int,
+                   Nq: int, Nkv: int, D: int, scale: float, window_tokens: int, sink_tokens: int = 0,
+                   dtype: int, layout: int, out, softmax_max=None, softmax_sum=None, stream=None) -> None:
+    """attn_fwd through a sliding window of the newest keys and the first `sink_tokens` keys (see
+    ``attn_fwd_sinks`` in include/attn.h)."""
+    lib = load_library()
+    nq, nk, nv, no, ns = _fwd_sizes(B, Sq, Skv, Nq, Nkv, D, D, layout)
+    et = _elem(dtype)
+    _check(lib.attn_fwd_sinks(_ptr(q, "q", nq, et), _ptr(k, "k", nk, et), _ptr(v, "v", nv, et),
+                              _cu_ptr(cu_seqlens_q, "cu_seqlens_q", B), _cu_ptr(cu_seqlens_kv, "cu_seqlens_kv", B),
+                              int(B), int(Sq), int(Skv), int(Nq), int(Nkv), int(D), float(scale),
+                              int(window_tokens), int(sink_tokens), int(dtype), int(layout),
+                              _ptr(out, "out", no, et), _ptr(softmax_max, "softmax_max", ns, "float32"),
+                              _ptr(softmax_sum, "softmax_sum", ns, "float32"), _stream(stream)), "attn_fwd_sinks")
+
+
+def _cache_ptr(x, name: str, num_pages: int, page_elems: int, page_stride: int, dtype: Optional[str]):
+    """Device data pointer of a page pool. Its pages must be dense; the pool itself may be a view with
+    gaps between the pages (one half of a [num_pages, 2, ...] tensor), whose distance must be
+    `page_stride`."""
+    if x is None or isinstance(x, int):
+        return _ptr(x, name)
+    stride = int(page_stride) or page_elems
+    if hasattr(x, "is_contiguous") and not x.is_contiguous():
+        if x.dim() < 2 or not x[0].is_contiguous():
+            raise ValueError(f"{name}: the elements of a page must be contiguous")
+        if x.stride(0) != stride:
+            raise ValueError(f"{name}: pages lie {x.stride(0)} elements apart, page_stride says {stride}")
+        if x.shape[0] < num_pages or x[0].numel() < page_elems:
+            raise ValueError(f"{name} holds {x.shape[0]} pages of {x[0].numel()} elements; the sizes given need "
+                             f"{num_pages} of {page_elems}")
+        x = x[0]
+        return _ptr(x, name, 0, dtype)
+    return _ptr(x, name, (num_pages - 1) * stride + page_elems if num_pages > 0 else 0, dtype)
+
+
+def attn_decode_workspace_size(*, Nq: int, Nkv: int, D: int, dtype: int) -> int:
+    """Bytes of the workspace of attn_decode_paged; allocate it with torch.zeros (uint8, on the device)."""
+    lib = load_library()
+    n = ctypes.c_int64(0)
+    _check(lib.attn_decode_workspace_size(int(Nq), int(Nkv), int(D), int(dtype), ctypes.byref(n)),
+           "attn_decode_workspace_size")
+    return int(n.value)
+
+
+def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, B: int, Nq: int, Nkv: int, D: int,
+                      num_pages: int, page_size: int, max_pages: int, page_stride: int = 0, scale: float,
+                      window_tokens: int = ATTN_WINDOW_ALL, sink_tokens: int = 0, dtype: int, layout: int,
+                      workspace, out, softmax_max=None, softmax_sum=None, stream=None) -> None:
+    """Attention of one new token per row over a paged key/value cache (see ``attn_decode_paged`` in
+    include/attn.h). `workspace` is a uint8 tensor of attn_decode_workspace_size bytes, zero-filled once."""
+    lib = load_library()
+    et, nq, pe = _elem(dtype), _n(B, Nq, D), _n(page_size, Nkv, D)
+    _check(lib.attn_decode_paged(_ptr(q, "q", nq, et), _cache_ptr(k_cache, "k_cache", num_pages, pe, page_stride, et),
+                                 _cache_ptr(v_cache, "v_cache", num_pages, pe, page_stride, et),
+                                 _ptr(page_table, "page_table", _n(B, max_pages), "int32"),
+                                 _ptr(seq_lens, "seq_lens", _n(B), "int32"), int(B), int(Nq), int(Nkv), int(D),
+                                 int(num_pages), int(page_size), int(max_pages), int(page_stride), float(scale),
+                                 int(window_tokens), int(sink_tokens), int(dtype), int(layout),
+                                 _ptr(workspace, "workspace", 0, "uint8"),
+                                 attn_decode_workspace_size(Nq=Nq, Nkv=Nkv, D=D, dtype=dtype)
+                                 if isinstance(workspace, int) else (0 if workspace is None else int(workspace.numel())),
+                                 _ptr(out, "out", nq, et), _ptr(softmax_max, "softmax_max", _n(B, Nq), "float32"),
+                                 _ptr(softmax_sum, "softmax_sum", _n(B, Nq), "float32"), _stream(stream)),
+           "attn_decode_paged")
+
+
+def attn_cache_append(k, v, page_table, seq_lens, k_cache, v_cache, *, cu_seqlens=None, T: int, B: int,
+                      Nkv: int, D: int, num_pages: int, page_size: int, max_pages: int, page_stride: int = 0,
+                      dtype: int, layout: int, stream=None) -> None:
+    """Write the keys and values of new tokens into a paged cache (see ``attn_cache_append`` in
+    include/attn.h)."""
+    lib = load_library()
+    et, nk, pe = _elem(dtype), _n(T, Nkv, D), _n(page_size, Nkv, D)
+    _check(lib.attn_cache_append(_ptr(k, "k", nk, et), _ptr(v, "v", nk, et),
+                                 _ptr(page_table, "page_table", _n(B, max_pages), "int32"),
+                                 _ptr(seq_lens, "seq_lens", _n(B), "int32"), _cu_ptr(cu_seqlens, "cu_seqlens", B),
+                                 int(T), int(B), int(Nkv), int(D), int(num_pages), int(page_size), int(max_pages),
+                                 int(page_stride), int(dtype), int(layout),
+                                 _cache_ptr(k_cache, "k_cache", num_pages, pe, page_stride, et),
+                                 _cache_ptr(v_cache, "v_cache", num_pages, pe, page_stride, et), _stream(stream)),
+           "attn_cache_append")
+
+
+def attn_cache_fork(page_table, src_rows, ref_count, page_table_out, ref_count_out, *, rows_in: int,
+                    rows_out: int, max_pages: int, num_pages: int, seq_lens=None, seq_lens_out=None,
+                    stream=None) -> None:
+    """Rows of a page table take the pages of other rows: fork, reorder, free (see ``attn_cache_fork``
+    in include/attn.h). The outputs may be the inputs."""
+    lib = load_library()
+    i32 = "int32"
+    _check(lib.attn_cache_fork(_ptr(page_table, "page_table", _n(rows_in, max_pages), i32),
+                               _ptr(src_rows, "src_rows", _n(rows_out), i32),
+                               _ptr(ref_count, "ref_count", _n(num_pages), i32),
+                               _ptr(seq_lens, "seq_lens", _n(rows_in), i32), int(rows_in), int(rows_out),
+                               int(max_pages), int(num_pages),
+                               _ptr(page_table_out, "page_table_out", _n(rows_out, max_pages), i32),
+                               _ptr(ref_count_out, "ref_count_out", _n(num_pages), i32),
+                               _ptr(seq_lens_out, "seq_lens_out", _n(rows_out), i32), _stream(stream)),
+           "attn_cache_fork")
+
+
+def attn_cache_reserve(page_table, ref_count, seq_lens, new_tokens, copies, *, B: int, max_pages: int,
+                       num_pages: int, page_size: int, stream=None) -> None:
+    """Give the rows pages of their own for their next tokens, in place (see ``attn_cache_reserve`` in
+    include/attn.h). `new_tokens` may be None (one per row)."""
+    lib = load_library()
+    i32 = "int32"
+    _check(lib.attn_cache_reserve(_ptr(page_table, "page_table", _n(B, max_pages), i32),
+                                  _ptr(ref_count, "ref_count", _n(num_pages), i32),
+                                  _ptr(seq_lens, "seq_lens", _n(B), i32), _ptr(new_tokens, "new_tokens", _n(B), i32),
+                                  int(B), int(max_pages), int(num_pages), int(page_size),
+                                  _ptr(copies, "copies", _n(B, 2), i32), _stream(stream)), "attn_cache_reserve")
+
+
+def attn_cache_compact(page_table, ref_count, page_table_out, ref_count_out, page_map, copies, live_pages, *,
+                       rows: int, max_pages: int, num_pages: int, stream=None) -> None:
+    """Plan the moves that bring all live pages to the front of the pool (see ``attn_cache_compact`` in
+    include/attn.h). page_table_out and ref_count_out may be the inputs."""
+    lib = load_library()
+    i32 = "int32"
+    _check(lib.attn_cache_compact(_ptr(page_table, "page_table", _n(rows, max_pages), i32),
+                                  _ptr(ref_count, "ref_count", _n(num_pages), i32), int(rows), int(max_pages),
+                                  int(num_pages), _ptr(page_table_out, "page_table_out", _n(rows, max_pages), i32),
+                                  _ptr(ref_count_out, "ref_count_out", _n(num_pages), i32),
+                                  _ptr(page_map, "page_map", _n(num_pages), i32),
+                                  _ptr(copies, "copies", 2 * (_n(num_pages) // 2), i32),
+                                  _ptr(live_pages, "live_pages", 1, i32), _stream(stream)), "attn_cache_compact")
+
+
+def attn_cache_copy(k_cache, v_cache, copies, *, n_copies: int, num_pages: int, page_elems: int,
+                    page_stride: int = 0, dtype: int, stream=None) -> None:
+    """Copy whole pages within a cache, as attn_cache_reserve and attn_cache_compact list them (see
+    ``attn_cache_copy`` in include/attn.h)."""
+    lib = load_library()
+    et = _elem(dtype)
+    _check(lib.attn_cache_copy(_ptr(copies, "copies", _n(n_copies, 2), "int32"), int(n_copies), int(num_pages),
+                               int(page_elems), int(page_stride), int(dtype),
+                               _cache_ptr(k_cache, "k_cache", num_pages, int(page_elems), page_stride, et),
+                               _cache_ptr(v_cache, "v_cache", num_pages, int(page_elems), page_stride, et),
+                               _stream(stream)), "attn_cache_copy")
 
 
 def attn_get_last_error(stream=None) -> int:

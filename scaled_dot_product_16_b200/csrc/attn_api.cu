@@ -67,7 +67,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 extern "C" {
 
-int attn_abi_version(void) { return (1 << 16) | 3; }  // 1.3: CSR plans (attn_csr_plan, ..._planned)
+int attn_abi_version(void) { return (1 << 16) | 4; }  // 1.4: attn_fwd_sinks, the paged cache calls
 
 const char* attn_status_string(int s) {
   switch (s) {
@@ -75,8 +75,9 @@ const char* attn_status_string(int s) {
     case ATTN_ERR_INVALID: return "invalid argument";
     case ATTN_ERR_UNSUPPORTED: return "unsupported by this library";
     case ATTN_ERR_CUDA: return "CUDA runtime error";
-    case ATTN_ERR_DATA: return "bad device data (cumulative lengths or CSR indices)";
+    case ATTN_ERR_DATA: return "bad device data (cumulative lengths, CSR indices or page tables)";
     case ATTN_ERR_TIMEOUT: return "pipeline wait timed out";
+    case ATTN_ERR_PAGES: return "not enough free pages";
     default: return "unknown status";
   }
 }
@@ -88,6 +89,8 @@ namespace {
 // The masked-call extras of fwd_impl (band limits, explicit mask, value head size).
 struct Extras {
   bool allow_band = false;
+  bool window = false;  // attn_fwd_sinks: `pre` holds window - 1
+  int64_t sinks = 0;
   int Dv = -1;  // -1: same as D
   int64_t pre = 0, next = 0;
   const uint8_t* mask = nullptr;
@@ -149,7 +152,8 @@ int fwd_impl(const void* q, const void* k, const void* v, const int32_t* cu_seql
   a.D = D;
   a.Dv = Dv;
   a.scale = scale;
-  a.mask_mode = mask_mode;
+  a.mask_mode = x.window ? sdpa::kMaskSinks : mask_mode;
+  a.sinks = clamp30(x.sinks);
   a.pre = clamp30(x.pre);
   a.next = clamp30(x.next);
   a.mask = x.mask;
@@ -210,6 +214,19 @@ int attn_fwd_masked(const void* q, const void* k, const void* v, const int32_t* 
   x.mask_rs = mask_row_stride;
   return fwd_impl(q, k, v, cu_seqlens_q, cu_seqlens_kv, B, Sq, Skv, Nq, Nkv, Dqk, scale, mask_mode,
                   dtype, layout, out, softmax_max, softmax_sum, 0, stream, x);
+}
+
+int attn_fwd_sinks(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
+                   const int32_t* cu_seqlens_kv, int B, int Sq, int Skv, int Nq, int Nkv, int D,
+                   float scale, int64_t window_tokens, int64_t sink_tokens, int dtype, int layout,
+                   void* out, float* softmax_max, float* softmax_sum, void* stream) {
+  if (window_tokens < 1 || sink_tokens < 0) return ATTN_ERR_INVALID;
+  Extras x;
+  x.window = true;
+  x.pre = window_tokens - 1;
+  x.sinks = sink_tokens;
+  return fwd_impl(q, k, v, cu_seqlens_q, cu_seqlens_kv, B, Sq, Skv, Nq, Nkv, D, scale,
+                  ATTN_MASK_CAUSAL_BOTTOMRIGHT, dtype, layout, out, softmax_max, softmax_sum, 0, stream, x);
 }
 
 int attn_sparse_csr(const float* q, const float* k, const float* v, const int32_t* csr_offset,
@@ -384,6 +401,237 @@ int attn_merge(const void* prev_out, const float* prev_max, const float* prev_su
   if (rc != ATTN_OK) return rc;
   const cudaError_t e = sdpa::launch_merge(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+int elem_size(int dtype) { return dtype == ATTN_F32 ? 4 : 2; }
+
+bool is_dtype(int dtype) { return dtype == ATTN_BF16 || dtype == ATTN_F32 || dtype == ATTN_F16; }
+
+// The sizes of a paged cache and its addressing. *page_stride = 0 stands for dense pages.
+int page_args(const int32_t* page_table, const int32_t* seq_lens, int B, int Nkv, int D, int num_pages,
+              int page_size, int max_pages, int64_t page_stride, int layout, sdpa::PagedArgs* p) {
+  if (layout != ATTN_BHSD && layout != ATTN_TND) return ATTN_ERR_INVALID;
+  if (B < 0 || Nkv < 1 || Nkv > 256 || D < 1 || D > 768) return ATTN_ERR_INVALID;
+  if (num_pages < 0 || page_size < 1 || max_pages < 0) return ATTN_ERR_INVALID;
+  const int64_t dense = (int64_t)page_size * Nkv * D;
+  if (page_stride != 0 && page_stride < dense) return ATTN_ERR_INVALID;
+  if (B > 0 && (seq_lens == nullptr || (page_table == nullptr && max_pages > 0))) return ATTN_ERR_INVALID;
+  if ((int64_t)max_pages * page_size > (int64_t(1) << 30)) return ATTN_ERR_UNSUPPORTED;  // positions
+  p->page_table = page_table;
+  p->seq_lens = seq_lens;
+  p->B = B;
+  p->num_pages = num_pages;
+  p->page_size = page_size;
+  p->max_pages = max_pages;
+  p->page_stride = page_stride != 0 ? page_stride : dense;
+  p->tok_stride = layout == ATTN_TND ? (int64_t)Nkv * D : D;
+  p->head_stride = layout == ATTN_TND ? D : (int64_t)page_size * D;
+  int l = 0;
+  while ((int64_t(1) << l) < page_size) ++l;
+  p->div_mul = (uint32_t)((((uint64_t(1) << l) - page_size) << 32) / page_size + 1);
+  p->div_shift = l;
+  return ATTN_OK;
+}
+
+constexpr int kMaxTableRows = 8192;
+
+int table_args(int rows, int max_pages, int num_pages) {
+  if (rows < 0 || max_pages < 0 || num_pages < 0) return ATTN_ERR_INVALID;
+  if (rows > kMaxTableRows || (int64_t)rows * max_pages > (int64_t(1) << 29)) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+int from_cuda(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+int attn_decode_workspace_size(int Nq, int Nkv, int D, int dtype, int64_t* bytes) {
+  if (bytes == nullptr || !is_dtype(dtype)) return ATTN_ERR_INVALID;
+  if (Nq < 1 || Nq > 256 || Nkv < 1 || Nq % Nkv != 0 || D < 1 || D > 768) return ATTN_ERR_INVALID;
+  if (D > 256) return ATTN_ERR_UNSUPPORTED;
+  *bytes = sdpa::decode_workspace_bytes(sdpa::decode_rows(dtype, Nq, Nkv, D), D);
+  return ATTN_OK;
+}
+
+int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                      const int32_t* seq_lens, int B, int Nq, int Nkv, int D, int num_pages, int page_size,
+                      int max_pages, int64_t page_stride, float scale, int64_t window_tokens,
+                      int64_t sink_tokens, int dtype, int layout, void* workspace, int64_t workspace_bytes,
+                      void* out, float* softmax_max, float* softmax_sum, void* stream) {
+  if (!is_dtype(dtype)) return ATTN_ERR_INVALID;
+  sdpa::DecodeArgs a{};
+  int rc = page_args(page_table, seq_lens, B, Nkv, D, num_pages, page_size, max_pages, page_stride, layout, &a.p);
+  if (rc != ATTN_OK) return rc;
+  if (window_tokens < 1 || sink_tokens < 0) return ATTN_ERR_INVALID;
+  if (!(scale > 0.f) || scale == INFINITY) return ATTN_ERR_INVALID;
+  if ((softmax_max == nullptr) != (softmax_sum == nullptr)) return ATTN_ERR_INVALID;
+  int64_t need = 0;
+  rc = attn_decode_workspace_size(Nq, Nkv, D, dtype, &need);
+  if (rc != ATTN_OK) return rc;
+  if (B == 0) return ATTN_OK;
+  if (q == nullptr || out == nullptr || workspace == nullptr) return ATTN_ERR_INVALID;
+  if (num_pages > 0 && (k_cache == nullptr || v_cache == nullptr)) return ATTN_ERR_INVALID;
+  if (workspace_bytes < need || !aligned16(workspace)) return ATTN_ERR_INVALID;
+  a.rows = sdpa::decode_rows(dtype, Nq, Nkv, D);
+  a.groups = (Nq / Nkv + a.rows - 1) / a.rows;
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.Nq = Nq;
+  a.Nkv = Nkv;
+  a.D = D;
+  a.dtype = dtype;
+  a.scale = scale;
+  a.window = clamp30(window_tokens);
+  a.sinks = clamp30(sink_tokens);
+  a.ctr = static_cast<unsigned*>(workspace);
+  a.part = reinterpret_cast<float*>(a.ctr + sdpa::kDecodeMaxCtas);
+  a.out = out;
+  a.smax = softmax_max;
+  a.ssum = softmax_sum;
+  rc = device_state(&a.status, &a.num_sms);
+  if (rc != ATTN_OK) return rc;
+  return from_cuda(sdpa::launch_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_cache_append(const void* k, const void* v, const int32_t* page_table, const int32_t* seq_lens,
+                      const int32_t* cu_seqlens, int T, int B, int Nkv, int D, int num_pages, int page_size,
+                      int max_pages, int64_t page_stride, int dtype, int layout, void* k_cache, void* v_cache,
+                      void* stream) {
+  if (!is_dtype(dtype)) return ATTN_ERR_INVALID;
+  sdpa::AppendArgs a{};
+  int rc = page_args(page_table, seq_lens, B, Nkv, D, num_pages, page_size, max_pages, page_stride, layout, &a.p);
+  if (rc != ATTN_OK) return rc;
+  if (T < 0 || (cu_seqlens == nullptr && T != B)) return ATTN_ERR_INVALID;
+  if (T == 0) return ATTN_OK;
+  if (B == 0) return ATTN_ERR_INVALID;
+  if (k == nullptr || v == nullptr || k_cache == nullptr || v_cache == nullptr) return ATTN_ERR_INVALID;
+  a.k_new = k;
+  a.v_new = v;
+  a.cu = cu_seqlens;
+  a.T = T;
+  a.Nkv = Nkv;
+  a.D = D;
+  a.dtype = dtype;
+  a.k = k_cache;
+  a.v = v_cache;
+  rc = device_state(&a.status, &a.num_sms);
+  if (rc != ATTN_OK) return rc;
+  return from_cuda(sdpa::launch_cache_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_cache_fork(const int32_t* page_table, const int32_t* src_rows, const int32_t* ref_count,
+                    const int32_t* seq_lens, int rows_in, int rows_out, int max_pages, int num_pages,
+                    int32_t* page_table_out, int32_t* ref_count_out, int32_t* seq_lens_out, void* stream) {
+  int rc = table_args(rows_in, max_pages, num_pages);
+  if (rc == ATTN_OK) rc = table_args(rows_out, max_pages, num_pages);
+  if (rc != ATTN_OK) return rc;
+  if ((seq_lens == nullptr) != (seq_lens_out == nullptr)) return ATTN_ERR_INVALID;
+  if (max_pages < 1) return ATTN_ERR_INVALID;
+  if (page_table_out != nullptr && page_table_out == page_table && rows_in != rows_out) return ATTN_ERR_INVALID;
+  if (rows_in > 0 && page_table == nullptr) return ATTN_ERR_INVALID;
+  if (rows_out > 0 && (src_rows == nullptr || page_table_out == nullptr)) return ATTN_ERR_INVALID;
+  if (num_pages > 0 && (ref_count == nullptr || ref_count_out == nullptr)) return ATTN_ERR_INVALID;
+  sdpa::ForkArgs a{};
+  a.table = page_table;
+  a.src = src_rows;
+  a.ref = ref_count;
+  a.lens = seq_lens;
+  a.rows_in = rows_in;
+  a.rows_out = rows_out;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.table_out = page_table_out;
+  a.ref_out = ref_count_out;
+  a.lens_out = seq_lens_out;
+  int sms = 0;
+  rc = device_state(&a.status, &sms);
+  if (rc != ATTN_OK) return rc;
+  return from_cuda(sdpa::launch_cache_fork(a, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_cache_reserve(int32_t* page_table, int32_t* ref_count, const int32_t* seq_lens,
+                       const int32_t* new_tokens, int B, int max_pages, int num_pages, int page_size,
+                       int32_t* copies, void* stream) {
+  int rc = table_args(B, max_pages, num_pages);
+  if (rc != ATTN_OK) return rc;
+  if (page_size < 1) return ATTN_ERR_INVALID;
+  if ((int64_t)max_pages * page_size > (int64_t(1) << 30)) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0) return ATTN_OK;
+  if (seq_lens == nullptr || copies == nullptr) return ATTN_ERR_INVALID;
+  if (max_pages > 0 && page_table == nullptr) return ATTN_ERR_INVALID;
+  if (num_pages > 0 && ref_count == nullptr) return ATTN_ERR_INVALID;
+  sdpa::ReserveArgs a{};
+  a.table = page_table;
+  a.ref = ref_count;
+  a.lens = seq_lens;
+  a.new_tokens = new_tokens;
+  a.copies = copies;
+  a.B = B;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  int sms = 0;
+  rc = device_state(&a.status, &sms);
+  if (rc != ATTN_OK) return rc;
+  return from_cuda(sdpa::launch_cache_reserve(a, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_cache_compact(const int32_t* page_table, const int32_t* ref_count, int rows, int max_pages,
+                       int num_pages, int32_t* page_table_out, int32_t* ref_count_out, int32_t* page_map,
+                       int32_t* copies, int32_t* live_pages, void* stream) {
+  const int rc0 = table_args(rows, max_pages, num_pages);
+  if (rc0 != ATTN_OK) return rc0;
+  const int64_t n = (int64_t)rows * max_pages;
+  if (live_pages == nullptr) return ATTN_ERR_INVALID;
+  if (n > 0 && (page_table == nullptr || page_table_out == nullptr)) return ATTN_ERR_INVALID;
+  if (num_pages > 0 && (ref_count == nullptr || ref_count_out == nullptr || page_map == nullptr))
+    return ATTN_ERR_INVALID;
+  if (num_pages > 1 && copies == nullptr) return ATTN_ERR_INVALID;
+  sdpa::CompactArgs a{};
+  a.table = page_table;
+  a.ref = ref_count;
+  a.rows = rows;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.table_out = page_table_out;
+  a.ref_out = ref_count_out;
+  a.page_map = page_map;
+  a.copies = copies;
+  a.live = live_pages;
+  int sms = 0;
+  const int rc = device_state(&a.status, &sms);
+  if (rc != ATTN_OK) return rc;
+  return from_cuda(sdpa::launch_cache_compact(a, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_cache_copy(const int32_t* copies, int n_copies, int num_pages, int64_t page_elems, int64_t page_stride,
+                    int dtype, void* k_cache, void* v_cache, void* stream) {
+  if (!is_dtype(dtype)) return ATTN_ERR_INVALID;
+  if (n_copies < 0 || num_pages < 0 || page_elems < 1) return ATTN_ERR_INVALID;
+  if (page_stride != 0 && page_stride < page_elems) return ATTN_ERR_INVALID;
+  if (n_copies == 0) return ATTN_OK;
+  if (copies == nullptr || (reinterpret_cast<uintptr_t>(copies) & 7u) != 0) return ATTN_ERR_INVALID;
+  if (num_pages > 0 && (k_cache == nullptr || v_cache == nullptr)) return ATTN_ERR_INVALID;
+  if (page_elems > (int64_t(1) << 34)) return ATTN_ERR_UNSUPPORTED;
+  const int64_t es = elem_size(dtype);
+  sdpa::PageCopyArgs a{};
+  a.copies = copies;
+  a.n = n_copies;
+  a.num_pages = num_pages;
+  a.page_bytes = page_elems * es;
+  a.stride_bytes = (page_stride != 0 ? page_stride : page_elems) * es;
+  a.k = k_cache;
+  a.v = v_cache;
+  const int rc = device_state(&a.status, &a.num_sms);
+  if (rc != ATTN_OK) return rc;
+  return from_cuda(sdpa::launch_cache_copy(a, static_cast<cudaStream_t>(stream)));
 }
 
 int attn_get_last_error(void* stream, int* device_status) {

@@ -37,6 +37,12 @@ __device__ __forceinline__ int visible_begin(int mask_mode, int i, int pre) {
   return i - pre > 0 ? i - pre : 0;
 }
 
+// First key of the window of attn_fwd_sinks (kMaskSinks) that ends at row i's position i + sk - sq.
+__device__ __forceinline__ int window_begin(int i, int sq, int sk, int pre) {
+  const int p = i + sk - sq;
+  return p > pre ? p - pre : 0;
+}
+
 // Find which query tile of a packed batch this block owns. Sequence b contributes
 // ceil(len_b / tile) tiles, in sequence order. Run by one full warp; all lanes get the answer.
 // Returns false if `x` is past the last tile. Also validates the cumulative lengths

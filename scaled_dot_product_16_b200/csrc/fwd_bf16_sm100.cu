@@ -149,7 +149,9 @@ struct Unit {
   int q0, sq, sk;    // first query token and query length of the sequence; its key length
   int row0;          // first row (within the sequence) of Q0
   int rows0, rows1;  // rows of Q0 and Q1 (rows1 <= 0: no second tile)
-  int jlo;           // first key tile (the band's first tile for row0; 0 otherwise)
+  int jlo;           // first key tile (the band's first tile for row0; 0 otherwise). With sinks: the
+                     // tiles left out between the sinks' tiles and the window's
+  int ns;            // with sinks: key tiles of the sinks (the item's first ns tiles)
   int n0, n1;        // key tiles from jlo up to Q0's / Q1's last visible key (n1 >= n0)
   int s1;            // Q1's first key tile, counted from jlo (0 except with the band)
 };
@@ -252,6 +254,12 @@ __host__ __device__ __forceinline__ int rows_per_item(const FwdArgs& a) {
   return pair_heads(a) ? kBM : kRowsPerBlock;
 }
 
+// The key tile that tile j of an item is.
+template <int EXT>
+__device__ __forceinline__ int key_tile(const Unit& U, int j) {
+  return EXT == 3 && j < U.ns ? j : U.jlo + j;
+}
+
 // Decodes item x. Items run query-head (pair) fastest; for BHSD the row blocks go by level (the
 // last row block of every sequence first), for TND sequence by sequence with each sequence's last
 // row block first, so that the heaviest items of a sequence come first. Run by one full warp;
@@ -310,6 +318,20 @@ __device__ __forceinline__ bool decode_unit(const FwdArgs& a, int units_per_seq,
   const int r1 = pair ? U.row0 : U.row0 + kBM;  // Q1's first row
   // Key tiles run from jlo to the tile holding each Q tile's last visible key; n0 and n1 count
   // tiles from jlo. With the band, Q1 starts at its own first tile: s1 tiles after jlo.
+  if constexpr (EXT == 3) {
+    // The first ns tiles hold the sinks, the others the window: item tile j is key tile j + jlo from
+    // ns on. Q1's own window begins at tile s1 (its rows lie behind Q0's).
+    const int w0 = window_begin(U.row0, U.sq, U.sk, a.pre);
+    const int w1 = has1 ? window_begin(r1, U.sq, U.sk, a.pre) : w0;
+    U.ns = (min(a.sinks, w1) + kBN - 1) / kBN;
+    U.jlo = max(w0 / kBN, U.ns) - U.ns;
+    const int end0 = visible_end(a.mask_mode, U.row0 + U.rows0 - 1, U.sq, U.sk);
+    const int end1 = has1 ? visible_end(a.mask_mode, r1 + U.rows1 - 1, U.sq, U.sk) : 0;
+    U.n0 = max((end0 + kBN - 1) / kBN - U.jlo, 0);
+    U.n1 = has1 ? max((end1 + kBN - 1) / kBN - U.jlo, 0) : U.n0;
+    U.s1 = max(w1 / kBN - U.jlo, U.ns);
+    return true;
+  }
   U.jlo = EXT >= 1 ? visible_begin(a.mask_mode, U.row0, a.pre) / kBN : 0;
   const int kv_end0 = visible_end(a.mask_mode, U.row0 + U.rows0 - 1, U.sq, U.sk, a.next);
   const int kv_end1 = has1 ? visible_end(a.mask_mode, r1 + U.rows1 - 1, U.sq, U.sk, a.next) : 0;
@@ -321,7 +343,8 @@ __device__ __forceinline__ bool decode_unit(const FwdArgs& a, int units_per_seq,
 
 // EXT: the masked-call features. 0: plain calls, whose softmax loop carries none of their code;
 // 1: the band's lower edge; 2: the band and an explicit mask (its bytes take registers that the
-// band alone does not need).
+// band alone does not need); 3: a window that ends at each row's position and the first keys
+// (attn_fwd_sinks), whose key tiles between the two are left out.
 //
 // Persistent: each block (one per SM) takes items one after another, from the scheduler slot
 // `sched` when there is one, else x = blockIdx.x + k * gridDim.x. The TMA warp decodes each item
@@ -433,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (r > 0 && !wait_bar(bar_addr(&bars->kv_empty[s]), (r - 1) & 1, abort, a.status)) return false;
               const uint32_t fb = bar_addr(&bars->kv_full[s]);
               mbar_arrive_expect_tx(fb, (i & 1) ? C::kTileBytesV : C::kTileBytes);
-              load_tile((i & 1) ? &tm_v : &tm_k, sKV + s * C::kTileBytes, fb, k0 + (U.jlo + (i >> 1)) * kBN, khead,
+              load_tile((i & 1) ? &tm_v : &tm_k, sKV + s * C::kTileBytes, fb,
+                        k0 + key_tile<EXT>(U, i >> 1) * kBN, khead,
                         (i & 1) ? C::kBoxesV : C::kBoxes);
               ++it;
               return true;
@@ -506,12 +530,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait_bar(bar_addr(&bars->unit_full[slot]), (k / kUnitSlots) & 1, abort, a.status))) break;
           const Unit* us = &bars->units[slot];
           const int ub = us->b, n0 = us->n0, n1 = us->n1, s1 = us->s1;
+          const int ns = EXT == 3 ? us->ns : 0;
+          const int first1 = EXT == 3 && ns > 0 ? 0 : s1;  // Q1's first key tile
           const bool has1 = us->rows1 > 0;
           mbar_arrive(bar_addr(&bars->unit_empty[slot]));
           if (ub < 0) break;
           if (n1 <= 0) continue;
-          // Q1 works on key tiles s1 .. n1-1 (s1 = 0 except with the band)
-          auto act1 = [&](int j) { return has1 && j >= s1; };
+          // Q1 works on key tiles s1 .. n1-1 (s1 = 0 except with the band), and those of the sinks
+          auto act1 = [&](int j) { return has1 && (j >= s1 || (EXT == 3 && j < ns)); };
           // after the S MMAs of the item's last key tile: Q may be overwritten once they have run
           auto after_s = [&](int t) {
             if (t == n1 - 1) mma_commit(bar_addr(&bars->q_empty));
@@ -555,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = wait_bar(bar_addr(&bars->p_ready[1]), pc1 & 1, abort, a.status))) break;
               ++pc1;
               tc_fence_after();
-              issue_pv(O1, S1, iv, j > s1);
+              issue_pv(O1, S1, iv, j > first1);
               if (j == n1 - 1) mma_commit(bar_addr(&bars->o_done[1]));
             }
             release(iv);
@@ -596,13 +622,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w.b < 0) break;
       const bool has1 = w.rows1 > 0;
       const int jlo = w.jlo;
-      const int j0 = q == 0 ? 0 : w.s1;              // this Q tile's key tiles: j0 .. n-1
+      const int ns = EXT == 3 ? w.ns : 0, s1 = w.s1;
+      const int j0 = q == 0 || (EXT == 3 && ns > 0) ? 0 : s1;  // this Q tile's key tiles: j0 .. n-1
       const int n = q == 0 ? w.n0 : (has1 ? w.n1 : 0);
       const bool pair = pair_heads(a);
       const int i = w.row0 + (pair ? 0 : q * kBM) + r;  // row within the sequence
       const int hq = w.h + (pair ? q : 0);              // query head of this Q tile
       const int lim = i < w.sq ? visible_end(a.mask_mode, i, w.sq, w.sk, a.next) : w.sk;
-      const int lo = EXT >= 1 && i < w.sq ? visible_begin(a.mask_mode, i, a.pre) : 0;
+      const int lo = EXT == 0 || i >= w.sq ? 0
+                     : EXT == 3            ? window_begin(i, w.sq, w.sk, a.pre)
+                                           : visible_begin(a.mask_mode, i, a.pre);
       // explicit mask row of this query (rows past the sequence read none)
       const uint8_t* mrow = nullptr;
       if constexpr (EXT == 2)
@@ -614,11 +643,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       if (q == 0 || has1) {
         for (int j = j0; j < n; ++j) {
+          if (EXT == 3 && q == 1 && j == ns && j < s1) j = s1;  // tiles before Q1's own window
           ok = __all_sync(0xffffffffu, wait_bar(bar_addr(&bars->s_full[q]), sfc & 1, abort, a.status));
           ++sfc;
           if (!ok) break;
           tc_fence_after();
-          const int kbase = (jlo + j) * kBN;
+          const int kbase = (EXT == 3 && j < ns ? j : jlo + j) * kBN;
           uint4 mk[EXT == 2 ? 8 : 1];
           if constexpr (EXT == 2) {
             // the mask bytes of this row's 128 keys (16 at a time when aligned and whole);
@@ -659,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < kBN; ++c)
                 if (c >= hi) s[c >> 5][c & 31] = -INFINITY;
             }
-          } else if constexpr (EXT == 1) {
+          } else if constexpr (EXT == 1 || EXT == 3) {
             // each edge on its own: a tile of a band wider than a tile holds at most one of them
             if (kbase + kBN > lim) {
               const int hi = lim - kbase;
@@ -669,9 +699,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (kbase < lo) {
               const int first = lo - kbase;  // this row's first visible column of the tile
+              const int sinks = EXT == 3 ? a.sinks - kbase : 0;  // columns below it are visible too
 #pragma unroll
               for (int c = 0; c < kBN; ++c)
-                if (c < first) s[c >> 5][c & 31] = -INFINITY;
+                if (c < first && (EXT != 3 || c >= sinks)) s[c >> 5][c & 31] = -INFINITY;
             }
           } else {
             if (kbase + kBN > lim || kbase < lo) {
@@ -978,17 +1009,20 @@ cudaError_t launch_hd(const FwdArgs& a, cudaStream_t st) {
   CUtensorMap tq, tk, tv;
   const uint64_t D = HD, Dv = HDV;
   bool ok;
+  // without keys no key tile is loaded; the maps still need a base and a row
+  const void* k = a.Skv > 0 ? a.k : a.q;
+  const void* v = a.Skv > 0 ? a.v : a.q;
+  const uint64_t tq_rows = a.Sq > 0 ? a.Sq : 1, tk_rows = a.Skv > 0 ? a.Skv : 1;
   if (a.layout == ATTN_BHSD) {
     // (d, s, b*h): rows of a head are contiguous
     ok = make_map(&tq, a.q, D, a.Sq, (uint64_t)a.B * a.Nq, D * 2, (uint64_t)a.Sq * D * 2, kBM, 1, F16) &&
-         make_map(&tk, a.k, D, a.Skv, (uint64_t)a.B * a.Nkv, D * 2, (uint64_t)a.Skv * D * 2, kBN, 1, F16) &&
-         make_map(&tv, a.v, Dv, a.Skv, (uint64_t)a.B * a.Nkv, Dv * 2, (uint64_t)a.Skv * Dv * 2, kBN, 1, F16);
+         make_map(&tk, k, D, tk_rows, (uint64_t)a.B * a.Nkv, D * 2, tk_rows * D * 2, kBN, 1, F16) &&
+         make_map(&tv, v, Dv, tk_rows, (uint64_t)a.B * a.Nkv, Dv * 2, tk_rows * Dv * 2, kBN, 1, F16);
   } else {
     // (d, head, token): a tile is 128 tokens of one head
-    const uint64_t tq_rows = a.Sq > 0 ? a.Sq : 1, tk_rows = a.Skv > 0 ? a.Skv : 1;
     ok = make_map(&tq, a.q, D, a.Nq, tq_rows, D * 2, (uint64_t)a.Nq * D * 2, 1, kBM, F16) &&
-         make_map(&tk, a.k, D, a.Nkv, tk_rows, D * 2, (uint64_t)a.Nkv * D * 2, 1, kBN, F16) &&
-         make_map(&tv, a.v, Dv, a.Nkv, tk_rows, Dv * 2, (uint64_t)a.Nkv * Dv * 2, 1, kBN, F16);
+         make_map(&tk, k, D, a.Nkv, tk_rows, D * 2, (uint64_t)a.Nkv * D * 2, 1, kBN, F16) &&
+         make_map(&tv, v, Dv, a.Nkv, tk_rows, Dv * 2, (uint64_t)a.Nkv * Dv * 2, 1, kBN, F16);
   }
   // the plain output has Q's layout with the value head size; the TMA stores write 32-row boxes
   CUtensorMap to = tq;  // not read by the kernel when the output is an accumulator
@@ -1002,14 +1036,20 @@ cudaError_t launch_hd(const FwdArgs& a, cudaStream_t st) {
   auto kernel = a.mask != nullptr                 ? fwd_bf16_kernel<HD, HDV, F16, 2>
                 : a.mask_mode == ATTN_MASK_BAND ? fwd_bf16_kernel<HD, HDV, F16, 1>
                                                 : fwd_bf16_kernel<HD, HDV, F16, 0>;
+  int which = a.mask != nullptr ? 2 : a.mask_mode == ATTN_MASK_BAND ? 1 : 0;
+  if constexpr (HD == HDV) {  // attn_fwd_sinks has one head size
+    if (a.mask_mode == kMaskSinks) {
+      kernel = fwd_bf16_kernel<HD, HDV, F16, 3>;
+      which = 3;
+    }
+  }
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   // The register split inside the kernel (softmax warpgroups up to kRegsSoftmax, the producer
   // warpgroup down to kRegsProducer) waits for registers the block must have been launched with:
   // refuse to launch a build whose kernel holds fewer than kRegsLaunch a thread.
   {
-    static std::atomic<int> checked[3] = {};
-    const int which = kernel == fwd_bf16_kernel<HD, HDV, F16, 2> ? 2 : kernel == fwd_bf16_kernel<HD, HDV, F16, 1> ? 1 : 0;
+    static std::atomic<int> checked[4] = {};
     if (checked[which].load(std::memory_order_acquire) == 0) {
       cudaFuncAttributes fa;
       e = cudaFuncGetAttributes(&fa, kernel);

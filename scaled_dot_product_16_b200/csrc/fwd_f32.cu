@@ -112,7 +112,10 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
 
   // keys needed by the tile: from the first row's first visible key to the last row's last
   const int kv_end = visible_end(a.mask_mode, row0 + nrows - 1, sq, sk, a.next);
-  const int kv_begin = visible_begin(a.mask_mode, row0, a.pre) / kBN * kBN;
+  const bool sinks = a.mask_mode == kMaskSinks;
+  const int kv_begin = (sinks ? window_begin(row0, sq, sk, a.pre) : visible_begin(a.mask_mode, row0, a.pre)) / kBN * kBN;
+  // attn_fwd_sinks: the tiles of the first keys come before those of the window
+  const int sink_end = sinks ? (min(a.sinks, kv_begin) + kBN - 1) / kBN * kBN : 0;
 
   constexpr int DT = DMAX / 32;  // head-dim columns per lane
   float acc[kRowsPerWarp][DT];
@@ -124,12 +127,12 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
     l[r] = 0.f;
     const int i = row0 + warp * kRowsPerWarp + r;
     vend[r] = i < sq ? visible_end(a.mask_mode, i, sq, sk, a.next) : 0;
-    vbeg[r] = visible_begin(a.mask_mode, i, a.pre);
+    vbeg[r] = sinks ? window_begin(i, sq, sk, a.pre) : visible_begin(a.mask_mode, i, a.pre);
 #pragma unroll
     for (int t = 0; t < DT; ++t) acc[r][t] = 0.f;
   }
 
-  for (int j0 = kv_begin; j0 < kv_end; j0 += kBN) {
+  for (int j0 = sink_end > 0 ? 0 : kv_begin; j0 < kv_end; j0 = j0 + kBN == sink_end ? kv_begin : j0 + kBN) {
     __syncthreads();  // previous tile fully consumed (and Q staged on the first pass)
     for (int x = threadIdx.x; x < kBN * D; x += blockDim.x) {
       const int r = x / D, d = x - r * D;
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
 #pragma unroll
     for (int r = 0; r < kRowsPerWarp; ++r) {
       const int i = row0 + warp * kRowsPerWarp + r;
-      bool vis = j >= vbeg[r] && j < vend[r];
+      bool vis = (j >= vbeg[r] || (sinks && j < a.sinks)) && j < vend[r];
       if (vis && mrow0 != nullptr) vis = mrow0[(int64_t)i * a.mask_rs + j] == 0;
       const float sc = vis ? s[r] * a.scale : -INFINITY;
       float mx = sc;

@@ -6,6 +6,10 @@
 
 namespace sdpa {
 
+// Internal mask mode of attn_fwd_sinks, beside the attn_mask values: row i at position
+// p = i + sk - sq sees key j iff j <= p and (j >= p - pre or j < sinks).
+constexpr int kMaskSinks = 4;
+
 struct FwdArgs {
   const void* q;
   const void* k;
@@ -16,7 +20,9 @@ struct FwdArgs {
   int Dv;  // value / output head size (== D except through attn_fwd_masked)
   float scale;
   int mask_mode, layout, dtype;
-  int pre, next;               // band limits (mask_mode ATTN_MASK_BAND), clamped to +-2^30
+  int pre, next;               // band limits (mask_mode ATTN_MASK_BAND), clamped to +-2^30;
+                               // kMaskSinks: pre = window - 1
+  int sinks;                   // kMaskSinks: first keys that stay visible
   const uint8_t* mask;         // explicit mask, 1 = excluded (null: none)
   int64_t mask_bs, mask_rs;    // its batch and row strides in bytes
   bool mask_vec;               // mask, mask_bs and mask_rs all 16-byte aligned
@@ -81,6 +87,102 @@ struct MergeArgs {
   int* status;
 };
 
+// A paged key/value cache (paged.cuh) and the rows of its page table.
+struct PagedArgs {
+  const int32_t* page_table;  // [B, max_pages]
+  const int32_t* seq_lens;    // [B]
+  int B, num_pages, page_size, max_pages;
+  int64_t page_stride, tok_stride, head_stride;  // elements
+  uint32_t div_mul;           // division by page_size (page_of)
+  int div_shift;
+};
+
+struct DecodeArgs {
+  PagedArgs p;
+  const void* q;  // [B, Nq, D]
+  const void* k;
+  const void* v;
+  int Nq, Nkv, D, dtype;
+  float scale;
+  int window, sinks;  // clamped to 2^30
+  int rows, groups;   // query heads a unit works on; units a KV head's query heads are cut into
+  float* part;        // workspace: partial results
+  unsigned* ctr;      // workspace: arrival counters, 0 between calls
+  void* out;          // [B, Nq, D]
+  float* smax;        // [B, Nq], may be null with ssum
+  float* ssum;
+  int* status;
+  int num_sms;
+};
+
+struct AppendArgs {
+  PagedArgs p;
+  const void* k_new;          // [T, Nkv, D]
+  const void* v_new;
+  const int32_t* cu;          // [B] cumulative new tokens, or null: one per row
+  int T, Nkv, D, dtype;
+  void* k;
+  void* v;
+  int* status;
+  int num_sms;
+};
+
+struct ForkArgs {
+  const int32_t* table;
+  const int32_t* src;
+  const int32_t* ref;
+  const int32_t* lens;      // may be null with lens_out
+  int rows_in, rows_out, max_pages, num_pages;
+  int32_t* table_out;
+  int32_t* ref_out;
+  int32_t* lens_out;
+  int* status;
+};
+
+struct ReserveArgs {
+  int32_t* table;
+  int32_t* ref;
+  const int32_t* lens;
+  const int32_t* new_tokens;  // null: one per row
+  int32_t* copies;            // [B, 2]
+  int B, max_pages, num_pages, page_size;
+  int* status;
+};
+
+struct CompactArgs {
+  const int32_t* table;
+  const int32_t* ref;
+  int rows, max_pages, num_pages;
+  int32_t* table_out;
+  int32_t* ref_out;
+  int32_t* page_map;  // [num_pages]
+  int32_t* copies;    // [num_pages / 2, 2]
+  int32_t* live;      // [1]
+  int* status;
+};
+
+struct PageCopyArgs {
+  const int32_t* copies;  // [n, 2]
+  int n, num_pages;
+  int64_t page_bytes, stride_bytes;
+  void* k;
+  void* v;
+  int* status;
+  int num_sms;
+};
+
+// Workspace of attn_decode_paged: partial results of at most kDecodeMaxCtas blocks (two each: the
+// unit a block's range starts in and the one it ends in) of `rows` query heads, and the counters.
+constexpr int kDecodeMaxCtas = 512;
+int decode_rows(int dtype, int Nq, int Nkv, int D);
+int64_t decode_workspace_bytes(int rows, int D);
+
+cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st);
+cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t st);
+cudaError_t launch_cache_reserve(const ReserveArgs& a, cudaStream_t st);
+cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st);
+cudaError_t launch_cache_copy(const PageCopyArgs& a, cudaStream_t st);
 cudaError_t launch_merge(const MergeArgs& a, cudaStream_t st);
 cudaError_t launch_fwd_f32(const FwdArgs& a, cudaStream_t st);
 cudaError_t launch_fwd_bf16(const FwdArgs& a, cudaStream_t st);

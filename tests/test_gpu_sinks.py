@@ -1,0 +1,149 @@
+"""attn_fwd_sinks on the GPU against the plain float64 form (tests/serving_ref.py). Tolerances are
+those of the other forward tests (tests/gpu_util.py); the arithmetic is the same kernels'."""
+import numpy as np
+import pytest
+import torch
+
+import scaled_dot_product_16_b200 as sdpa
+from scaled_dot_product_16_b200 import workloads as W
+from tests import gpu_util as G
+from tests import serving_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+IDS = {BF: "bf16", F16: "f16", F32: "f32"}.get
+
+
+def _run(inp, window, sinks, stats=True, dev=None):
+    q, k, v, cq, ck = dev if dev is not None else G.to_dev(inp)
+    out = G.Guarded(tuple(q.shape), q.dtype)
+    shape = tuple(q.shape[:-1])
+    m = G.Guarded(shape, F32) if stats else None
+    l = G.Guarded(shape, F32) if stats else None
+    sdpa.attn_fwd_sinks(q, k, v, cu_seqlens_q=cq, cu_seqlens_kv=ck, B=inp.B, Sq=inp.Sq, Skv=inp.Skv, Nq=inp.Nq,
+                        Nkv=inp.Nkv, D=inp.D, scale=inp.scale, window_tokens=window, sink_tokens=sinks, dtype=inp.dtype,
+                        layout=inp.layout, out=out.t, softmax_max=m.t if stats else None,
+                        softmax_sum=l.t if stats else None)
+    assert sdpa.attn_get_last_error() == 0
+    for g in (out, m, l):
+        if g is not None:
+            g.check()
+    return out.t.cpu(), (m.t.cpu() if stats else None), (l.t.cpu() if stats else None)
+
+
+def _check(inp, window, sinks):
+    out, m, l = _run(inp, window, sinks)
+    ref, rm, rl, A = R.window_fwd(inp, window, sinks)
+    G.check_out(G.f64(out), ref, inp.dtype, abs_ref=A)
+    G.check_stats(m.numpy(), l.numpy(), rm, rl)
+
+
+SPANS = [(1, 0), (1, 3), (64, 4), (127, 130), (128, 128), (129, 1), (300, 7), (5, 100000), (1 << 40, 0)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F16, F32], ids=IDS)
+@pytest.mark.parametrize("window,sinks", SPANS)
+def test_dense(dtype, window, sinks):
+    inp = W.dense_bhsd(1, 2, 700, 64, causal=False, dtype=dtype, seed=window % 91 + sinks % 17, cfg=72)
+    _check(inp, window, sinks)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=IDS)
+@pytest.mark.parametrize("Sq,Skv", [(1, 900), (130, 1000), (257, 1290), (400, 90), (300, 0), (1, 1)])
+@pytest.mark.parametrize("heads", [(2, 2), (4, 1), (6, 2)])
+def test_chunks_and_rows_without_keys(dtype, Sq, Skv, heads):
+    inp = W.dense_bhsd(2, heads[0], Sq, 128, causal=False, dtype=dtype, seed=Sq + Skv, cfg=73, Skv=Skv, Hkv=heads[1])
+    _check(inp, 200, 5)
+    _check(inp, 150, 300)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16, F32], ids=IDS)
+@pytest.mark.parametrize("heads", [(8, 2), (3, 3)])
+def test_varlen(dtype, heads):
+    inp = W.varlen_tnd([0, 700, 1, 257, 513, 0], *heads, 128, causal=False, dtype=dtype, seed=3, cfg=74)
+    _check(inp, 100, 4)
+    _check(inp, 256, 0)
+
+
+def test_varlen_with_longer_keys():
+    lq, lk = [5, 0, 300, 1], [905, 40, 640, 1]
+    a = W.varlen_tnd(lq, 4, 2, 64, causal=False, dtype=BF, seed=5, cfg=75)
+    b = W.varlen_tnd(lk, 4, 2, 64, causal=False, dtype=BF, seed=6, cfg=75)
+    a.k, a.v, a.Skv, a.cu_kv = b.k, b.v, b.Skv, b.cu_kv
+    _check(a, 130, 20)
+
+
+@pytest.mark.parametrize("D", [1, 33, 80, 256])
+def test_f32_head_sizes(D):
+    _check(W.dense_bhsd(1, 2, 150, D, causal=False, dtype=F32, seed=D, cfg=76), 40, 3)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16, F32], ids=IDS)
+def test_a_window_of_every_key_is_the_causal_forward_bit_for_bit(dtype):
+    inp = W.varlen_tnd([300, 0, 513], 4, 2, 128, causal=True, dtype=dtype, seed=4, cfg=77,
+                       mask_mode=W.MASK_CAUSAL_BOTTOMRIGHT)
+    a = G.run_fwd(inp)
+    for window, sinks in ((sdpa.ATTN_WINDOW_ALL, 0), (513, 0), (7, 1 << 40)):
+        for x, y in zip(a, _run(inp, window, sinks)):
+            assert torch.equal(x, y), (window, sinks)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=IDS)
+def test_keys_left_out_may_hold_anything(dtype):
+    """A chunk of 256 rows at positions 2048 .. 2303, window 128, 3 sinks: the key tiles between the
+    sinks' tile and the first window are never read."""
+    inp = W.dense_bhsd(1, 2, 256, 128, causal=False, dtype=dtype, seed=8, cfg=78, Skv=2304)
+    want = _run(inp, 128, 3)
+    inp.k[:, :, 128:1920] = float("nan")
+    inp.v[:, :, 128:1920] = float("inf")
+    inp.k[:, :, 1920:1921] = float("nan")   # position 1920 = 2048 - 128: in a tile that is read, seen by no row
+    for x, y in zip(want, _run(inp, 128, 3)):
+        assert torch.equal(x, y)
+
+
+def test_large_scores_and_one_hot_rows():
+    inp = W.dense_bhsd(1, 2, 300, 64, causal=False, dtype=BF, seed=9, cfg=79)
+    inp.q = inp.q * 64
+    _check(inp, 90, 2)
+
+
+def test_no_statistics_graph_replay_and_two_streams():
+    inp = W.varlen_tnd([300, 129, 800], 8, 2, 128, causal=False, dtype=BF, seed=10, cfg=80)
+    dev = G.to_dev(inp)
+    want = _run(inp, 200, 4, dev=dev)[0]
+    assert torch.equal(_run(inp, 200, 4, stats=False, dev=dev)[0], want)
+    q, k, v, cq, ck = dev
+    kw = dict(cu_seqlens_q=cq, cu_seqlens_kv=ck, B=inp.B, Sq=inp.Sq, Skv=inp.Skv, Nq=8, Nkv=2, D=128, scale=inp.scale,
+              window_tokens=200, sink_tokens=4, dtype=inp.dtype, layout=inp.layout)
+    outs = [torch.empty_like(q) for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for s, o in zip(streams, outs):
+        with torch.cuda.stream(s):
+            for _ in range(3):
+                sdpa.attn_fwd_sinks(q, k, v, out=o, **kw)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sdpa.attn_fwd_sinks(q, k, v, out=outs[2], **kw)
+    outs[2].zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o.cpu(), want)
+
+
+def test_bad_lengths_are_reported():
+    inp = W.varlen_tnd([100, 50], 2, 2, 64, causal=False, dtype=BF, seed=11, cfg=81)
+    q, k, v, cq, ck = G.to_dev(inp)
+    out = torch.empty_like(q)
+    kw = dict(B=2, Sq=150, Skv=150, Nq=2, Nkv=2, D=64, scale=0.125, window_tokens=9, sink_tokens=1, dtype=inp.dtype,
+              layout=inp.layout, out=out)
+    bad = torch.tensor([120, 100], dtype=torch.int32, device="cuda")
+    sdpa.attn_fwd_sinks(q, k, v, cu_seqlens_q=bad, cu_seqlens_kv=ck, **kw)
+    assert sdpa.attn_get_last_error() == sdpa.ATTN_ERR_DATA
+    sdpa.attn_fwd_sinks(q, k, v, cu_seqlens_q=cq, cu_seqlens_kv=bad, **kw)
+    assert sdpa.attn_get_last_error() == sdpa.ATTN_ERR_DATA
+    sdpa.attn_fwd_sinks(q, k, v, cu_seqlens_q=cq, cu_seqlens_kv=ck, **kw)
+    assert sdpa.attn_get_last_error() == 0
