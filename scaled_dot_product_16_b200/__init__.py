@@ -352,30 +352,70 @@ def attn_merge(prev_out, prev_max, prev_sum, cur_out, cur_max, cur_sum, *, S: in
                           _ptr(out_sum, "out_sum", ns, f), _stream(stream)), "attn_merge")
 
 
+# The serving calls are made once a layer and token, so what the binding adds to a call's latency
+# counts: the checks of _ptr in the few attribute reads that a tensor in order needs, and _ptr itself,
+# with its messages, for everything else.
+_DEV = {}
+
+
+def _tools():
+    """What the fast checks need of torch: its tensor type, dtypes by code, device and raw stream getters."""
+    import torch
+    _DEV.update(tensor=torch.Tensor, elem={ATTN_BF16: torch.bfloat16, ATTN_F32: torch.float32, ATTN_F16: torch.float16},
+                f32=torch.float32, i32=torch.int32, u8=torch.uint8, device=torch._C._cuda_getDevice,
+                stream=torch._C._cuda_getCurrentRawStream)
+    return _DEV
+
+
+def _here() -> int:
+    """The current CUDA device, or -1 where there is none (every tensor then goes through _ptr)."""
+    try:
+        return (_DEV or _tools())["device"]()
+    except Exception:
+        return -1
+
+
+def _arg(x, name: str, numel: int, dt, dev: int) -> Optional[int]:
+    """_ptr for a tensor that is expected to be in order: on device `dev`, dense, of torch dtype `dt`,
+    with `numel` elements or more."""
+    if (type(x) is _DEV["tensor"] and x.dtype is dt and x.get_device() == dev and x.is_contiguous()
+            and x.numel() >= numel):
+        return x.data_ptr()
+    return _ptr(x, name, max(numel, 0), str(dt).replace("torch.", "") if dt is not None else None)
+
+
+def _on(stream, dev: int) -> Optional[int]:
+    """The stream to launch on, as _stream gives it."""
+    if stream is None and dev >= 0:
+        return _DEV["stream"](dev)
+    return _stream(stream)
+
+
 def attn_fwd_sinks(q, k, v, *, cu_seqlens_q=None, cu_seqlens_kv=None, B: int, Sq: int, Skv: int,
                    Nq: int, Nkv: int, D: int, scale: float, window_tokens: int, sink_tokens: int = 0,
                    dtype: int, layout: int, out, softmax_max=None, softmax_sum=None, stream=None) -> None:
     """attn_fwd through a sliding window of the newest keys and the first `sink_tokens` keys (see
     ``attn_fwd_sinks`` in include/attn.h)."""
-    lib = load_library()
-    nq, nk, nv, no, ns = _fwd_sizes(B, Sq, Skv, Nq, Nkv, D, D, layout)
-    et = _elem(dtype)
-    _check(lib.attn_fwd_sinks(_ptr(q, "q", nq, et), _ptr(k, "k", nk, et), _ptr(v, "v", nv, et),
-                              _cu_ptr(cu_seqlens_q, "cu_seqlens_q", B), _cu_ptr(cu_seqlens_kv, "cu_seqlens_kv", B),
-                              int(B), int(Sq), int(Skv), int(Nq), int(Nkv), int(D), float(scale),
-                              int(window_tokens), int(sink_tokens), int(dtype), int(layout),
-                              _ptr(out, "out", no, et), _ptr(softmax_max, "softmax_max", ns, "float32"),
-                              _ptr(softmax_sum, "softmax_sum", ns, "float32"), _stream(stream)), "attn_fwd_sinks")
+    lib, dev = _lib or load_library(), _here()
+    nq, nk, _, no, ns = _fwd_sizes(B, Sq, Skv, Nq, Nkv, D, D, layout)
+    et, f32, i32 = _DEV["elem"].get(dtype), _DEV["f32"], _DEV["i32"]
+    rc = lib.attn_fwd_sinks(
+        _arg(q, "q", nq, et, dev), _arg(k, "k", nk, et, dev), _arg(v, "v", nk, et, dev),
+        None if cu_seqlens_q is None else _arg(cu_seqlens_q, "cu_seqlens_q", B, i32, dev),
+        None if cu_seqlens_kv is None else _arg(cu_seqlens_kv, "cu_seqlens_kv", B, i32, dev), B, Sq, Skv, Nq, Nkv, D,
+        scale, window_tokens, sink_tokens, dtype, layout, _arg(out, "out", no, et, dev),
+        None if softmax_max is None else _arg(softmax_max, "softmax_max", ns, f32, dev),
+        None if softmax_sum is None else _arg(softmax_sum, "softmax_sum", ns, f32, dev), _on(stream, dev))
+    if rc:
+        _check(rc, "attn_fwd_sinks")
 
 
-def _cache_ptr(x, name: str, num_pages: int, page_elems: int, page_stride: int, dtype: Optional[str]):
+def _pool(x, name: str, num_pages: int, page_elems: int, page_stride: int, dt, dev: int):
     """Device data pointer of a page pool. Its pages must be dense; the pool itself may be a view with
     gaps between the pages (one half of a [num_pages, 2, ...] tensor), whose distance must be
     `page_stride`."""
-    if x is None or isinstance(x, int):
-        return _ptr(x, name)
-    stride = int(page_stride) or page_elems
-    if hasattr(x, "is_contiguous") and not x.is_contiguous():
+    stride = page_stride or page_elems
+    if x is not None and not isinstance(x, int) and not x.is_contiguous():
         if x.dim() < 2 or not x[0].is_contiguous():
             raise ValueError(f"{name}: the elements of a page must be contiguous")
         if x.stride(0) != stride:
@@ -383,9 +423,8 @@ def _cache_ptr(x, name: str, num_pages: int, page_elems: int, page_stride: int, 
         if x.shape[0] < num_pages or x[0].numel() < page_elems:
             raise ValueError(f"{name} holds {x.shape[0]} pages of {x[0].numel()} elements; the sizes given need "
                              f"{num_pages} of {page_elems}")
-        x = x[0]
-        return _ptr(x, name, 0, dtype)
-    return _ptr(x, name, (num_pages - 1) * stride + page_elems if num_pages > 0 else 0, dtype)
+        return _arg(x[0], name, 0, dt, dev)
+    return _arg(x, name, (num_pages - 1) * stride + page_elems if num_pages > 0 else 0, dt, dev)
 
 
 def attn_decode_workspace_size(*, Nq: int, Nkv: int, D: int, dtype: int) -> int:
@@ -403,20 +442,26 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, B: int, Nq: 
                       workspace, out, softmax_max=None, softmax_sum=None, stream=None) -> None:
     """Attention of one new token per row over a paged key/value cache (see ``attn_decode_paged`` in
     include/attn.h). `workspace` is a uint8 tensor of attn_decode_workspace_size bytes, zero-filled once."""
-    lib = load_library()
-    et, nq, pe = _elem(dtype), _n(B, Nq, D), _n(page_size, Nkv, D)
-    _check(lib.attn_decode_paged(_ptr(q, "q", nq, et), _cache_ptr(k_cache, "k_cache", num_pages, pe, page_stride, et),
-                                 _cache_ptr(v_cache, "v_cache", num_pages, pe, page_stride, et),
-                                 _ptr(page_table, "page_table", _n(B, max_pages), "int32"),
-                                 _ptr(seq_lens, "seq_lens", _n(B), "int32"), int(B), int(Nq), int(Nkv), int(D),
-                                 int(num_pages), int(page_size), int(max_pages), int(page_stride), float(scale),
-                                 int(window_tokens), int(sink_tokens), int(dtype), int(layout),
-                                 _ptr(workspace, "workspace", 0, "uint8"),
-                                 attn_decode_workspace_size(Nq=Nq, Nkv=Nkv, D=D, dtype=dtype)
-                                 if isinstance(workspace, int) else (0 if workspace is None else int(workspace.numel())),
-                                 _ptr(out, "out", nq, et), _ptr(softmax_max, "softmax_max", _n(B, Nq), "float32"),
-                                 _ptr(softmax_sum, "softmax_sum", _n(B, Nq), "float32"), _stream(stream)),
-           "attn_decode_paged")
+    lib, dev = _lib or load_library(), _here()
+    et, f32, i32 = _DEV["elem"].get(dtype), _DEV["f32"], _DEV["i32"]
+    nq, pe = B * Nq * D, page_size * Nkv * D
+    ws = _arg(workspace, "workspace", 0, _DEV["u8"], dev)
+    if workspace is None:
+        ws_bytes = 0
+    elif isinstance(workspace, int):
+        ws_bytes = attn_decode_workspace_size(Nq=Nq, Nkv=Nkv, D=D, dtype=dtype)
+    else:
+        ws_bytes = workspace.numel()
+    rc = lib.attn_decode_paged(
+        _arg(q, "q", nq, et, dev), _pool(k_cache, "k_cache", num_pages, pe, page_stride, et, dev),
+        _pool(v_cache, "v_cache", num_pages, pe, page_stride, et, dev),
+        _arg(page_table, "page_table", B * max_pages, i32, dev), _arg(seq_lens, "seq_lens", B, i32, dev), B, Nq, Nkv, D,
+        num_pages, page_size, max_pages, page_stride, scale, window_tokens, sink_tokens, dtype, layout, ws, ws_bytes,
+        _arg(out, "out", nq, et, dev),
+        None if softmax_max is None else _arg(softmax_max, "softmax_max", B * Nq, f32, dev),
+        None if softmax_sum is None else _arg(softmax_sum, "softmax_sum", B * Nq, f32, dev), _on(stream, dev))
+    if rc:
+        _check(rc, "attn_decode_paged")
 
 
 def attn_cache_append(k, v, page_table, seq_lens, k_cache, v_cache, *, cu_seqlens=None, T: int, B: int,
@@ -424,16 +469,17 @@ def attn_cache_append(k, v, page_table, seq_lens, k_cache, v_cache, *, cu_seqlen
                       dtype: int, layout: int, stream=None) -> None:
     """Write the keys and values of new tokens into a paged cache (see ``attn_cache_append`` in
     include/attn.h)."""
-    lib = load_library()
-    et, nk, pe = _elem(dtype), _n(T, Nkv, D), _n(page_size, Nkv, D)
-    _check(lib.attn_cache_append(_ptr(k, "k", nk, et), _ptr(v, "v", nk, et),
-                                 _ptr(page_table, "page_table", _n(B, max_pages), "int32"),
-                                 _ptr(seq_lens, "seq_lens", _n(B), "int32"), _cu_ptr(cu_seqlens, "cu_seqlens", B),
-                                 int(T), int(B), int(Nkv), int(D), int(num_pages), int(page_size), int(max_pages),
-                                 int(page_stride), int(dtype), int(layout),
-                                 _cache_ptr(k_cache, "k_cache", num_pages, pe, page_stride, et),
-                                 _cache_ptr(v_cache, "v_cache", num_pages, pe, page_stride, et), _stream(stream)),
-           "attn_cache_append")
+    lib, dev = _lib or load_library(), _here()
+    et, i32 = _DEV["elem"].get(dtype), _DEV["i32"]
+    nk, pe = T * Nkv * D, page_size * Nkv * D
+    rc = lib.attn_cache_append(
+        _arg(k, "k", nk, et, dev), _arg(v, "v", nk, et, dev), _arg(page_table, "page_table", B * max_pages, i32, dev),
+        _arg(seq_lens, "seq_lens", B, i32, dev),
+        None if cu_seqlens is None else _arg(cu_seqlens, "cu_seqlens", B, i32, dev), T, B, Nkv, D, num_pages, page_size,
+        max_pages, page_stride, dtype, layout, _pool(k_cache, "k_cache", num_pages, pe, page_stride, et, dev),
+        _pool(v_cache, "v_cache", num_pages, pe, page_stride, et, dev), _on(stream, dev))
+    if rc:
+        _check(rc, "attn_cache_append")
 
 
 def attn_cache_fork(page_table, src_rows, ref_count, page_table_out, ref_count_out, *, rows_in: int,
@@ -441,58 +487,62 @@ def attn_cache_fork(page_table, src_rows, ref_count, page_table_out, ref_count_o
                     stream=None) -> None:
     """Rows of a page table take the pages of other rows: fork, reorder, free (see ``attn_cache_fork``
     in include/attn.h). The outputs may be the inputs."""
-    lib = load_library()
-    i32 = "int32"
-    _check(lib.attn_cache_fork(_ptr(page_table, "page_table", _n(rows_in, max_pages), i32),
-                               _ptr(src_rows, "src_rows", _n(rows_out), i32),
-                               _ptr(ref_count, "ref_count", _n(num_pages), i32),
-                               _ptr(seq_lens, "seq_lens", _n(rows_in), i32), int(rows_in), int(rows_out),
-                               int(max_pages), int(num_pages),
-                               _ptr(page_table_out, "page_table_out", _n(rows_out, max_pages), i32),
-                               _ptr(ref_count_out, "ref_count_out", _n(num_pages), i32),
-                               _ptr(seq_lens_out, "seq_lens_out", _n(rows_out), i32), _stream(stream)),
-           "attn_cache_fork")
+    lib, dev = _lib or load_library(), _here()
+    i32 = _DEV["i32"]
+    rc = lib.attn_cache_fork(
+        _arg(page_table, "page_table", rows_in * max_pages, i32, dev), _arg(src_rows, "src_rows", rows_out, i32, dev),
+        _arg(ref_count, "ref_count", num_pages, i32, dev),
+        None if seq_lens is None else _arg(seq_lens, "seq_lens", rows_in, i32, dev), rows_in, rows_out, max_pages,
+        num_pages, _arg(page_table_out, "page_table_out", rows_out * max_pages, i32, dev),
+        _arg(ref_count_out, "ref_count_out", num_pages, i32, dev),
+        None if seq_lens_out is None else _arg(seq_lens_out, "seq_lens_out", rows_out, i32, dev), _on(stream, dev))
+    if rc:
+        _check(rc, "attn_cache_fork")
 
 
 def attn_cache_reserve(page_table, ref_count, seq_lens, new_tokens, copies, *, B: int, max_pages: int,
                        num_pages: int, page_size: int, stream=None) -> None:
     """Give the rows pages of their own for their next tokens, in place (see ``attn_cache_reserve`` in
     include/attn.h). `new_tokens` may be None (one per row)."""
-    lib = load_library()
-    i32 = "int32"
-    _check(lib.attn_cache_reserve(_ptr(page_table, "page_table", _n(B, max_pages), i32),
-                                  _ptr(ref_count, "ref_count", _n(num_pages), i32),
-                                  _ptr(seq_lens, "seq_lens", _n(B), i32), _ptr(new_tokens, "new_tokens", _n(B), i32),
-                                  int(B), int(max_pages), int(num_pages), int(page_size),
-                                  _ptr(copies, "copies", _n(B, 2), i32), _stream(stream)), "attn_cache_reserve")
+    lib, dev = _lib or load_library(), _here()
+    i32 = _DEV["i32"]
+    rc = lib.attn_cache_reserve(
+        _arg(page_table, "page_table", B * max_pages, i32, dev), _arg(ref_count, "ref_count", num_pages, i32, dev),
+        _arg(seq_lens, "seq_lens", B, i32, dev),
+        None if new_tokens is None else _arg(new_tokens, "new_tokens", B, i32, dev), B, max_pages, num_pages, page_size,
+        _arg(copies, "copies", 2 * B, i32, dev), _on(stream, dev))
+    if rc:
+        _check(rc, "attn_cache_reserve")
 
 
 def attn_cache_compact(page_table, ref_count, page_table_out, ref_count_out, page_map, copies, live_pages, *,
                        rows: int, max_pages: int, num_pages: int, stream=None) -> None:
     """Plan the moves that bring all live pages to the front of the pool (see ``attn_cache_compact`` in
     include/attn.h). page_table_out and ref_count_out may be the inputs."""
-    lib = load_library()
-    i32 = "int32"
-    _check(lib.attn_cache_compact(_ptr(page_table, "page_table", _n(rows, max_pages), i32),
-                                  _ptr(ref_count, "ref_count", _n(num_pages), i32), int(rows), int(max_pages),
-                                  int(num_pages), _ptr(page_table_out, "page_table_out", _n(rows, max_pages), i32),
-                                  _ptr(ref_count_out, "ref_count_out", _n(num_pages), i32),
-                                  _ptr(page_map, "page_map", _n(num_pages), i32),
-                                  _ptr(copies, "copies", 2 * (_n(num_pages) // 2), i32),
-                                  _ptr(live_pages, "live_pages", 1, i32), _stream(stream)), "attn_cache_compact")
+    lib, dev = _lib or load_library(), _here()
+    i32 = _DEV["i32"]
+    rc = lib.attn_cache_compact(
+        _arg(page_table, "page_table", rows * max_pages, i32, dev), _arg(ref_count, "ref_count", num_pages, i32, dev),
+        rows, max_pages, num_pages, _arg(page_table_out, "page_table_out", rows * max_pages, i32, dev),
+        _arg(ref_count_out, "ref_count_out", num_pages, i32, dev), _arg(page_map, "page_map", num_pages, i32, dev),
+        _arg(copies, "copies", 2 * (num_pages // 2), i32, dev), _arg(live_pages, "live_pages", 1, i32, dev),
+        _on(stream, dev))
+    if rc:
+        _check(rc, "attn_cache_compact")
 
 
 def attn_cache_copy(k_cache, v_cache, copies, *, n_copies: int, num_pages: int, page_elems: int,
                     page_stride: int = 0, dtype: int, stream=None) -> None:
     """Copy whole pages within a cache, as attn_cache_reserve and attn_cache_compact list them (see
     ``attn_cache_copy`` in include/attn.h)."""
-    lib = load_library()
-    et = _elem(dtype)
-    _check(lib.attn_cache_copy(_ptr(copies, "copies", _n(n_copies, 2), "int32"), int(n_copies), int(num_pages),
-                               int(page_elems), int(page_stride), int(dtype),
-                               _cache_ptr(k_cache, "k_cache", num_pages, int(page_elems), page_stride, et),
-                               _cache_ptr(v_cache, "v_cache", num_pages, int(page_elems), page_stride, et),
-                               _stream(stream)), "attn_cache_copy")
+    lib, dev = _lib or load_library(), _here()
+    et = _DEV["elem"].get(dtype)
+    rc = lib.attn_cache_copy(
+        _arg(copies, "copies", 2 * n_copies, _DEV["i32"], dev), n_copies, num_pages, page_elems, page_stride, dtype,
+        _pool(k_cache, "k_cache", num_pages, page_elems, page_stride, et, dev),
+        _pool(v_cache, "v_cache", num_pages, page_elems, page_stride, et, dev), _on(stream, dev))
+    if rc:
+        _check(rc, "attn_cache_copy")
 
 
 def attn_get_last_error(stream=None) -> int:

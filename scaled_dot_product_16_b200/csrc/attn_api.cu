@@ -491,7 +491,7 @@ int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, c
   a.window = clamp30(window_tokens);
   a.sinks = clamp30(sink_tokens);
   a.ctr = static_cast<unsigned*>(workspace);
-  a.part = reinterpret_cast<float*>(a.ctr + sdpa::kDecodeMaxCtas);
+  a.part = reinterpret_cast<float*>(a.ctr + 2 * sdpa::kDecodeMaxCtas);
   a.out = out;
   a.smax = softmax_max;
   a.ssum = softmax_sum;

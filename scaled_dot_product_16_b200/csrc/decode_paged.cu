@@ -17,6 +17,7 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "paged.cuh"
@@ -28,6 +29,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kWarpKeys = 16;                // keys of a tile that one warp works on
 constexpr int kTile = kWarps * kWarpKeys;    // keys per tile
+constexpr int kJoin = 16;                    // parts of a unit that one block joins
 constexpr int kGenericRows = 4;              // query heads of a unit outside the tensor-core kernel
 
 // The blocks' ranges of the T tiles: the first T % n blocks have one more than the others.
@@ -180,13 +182,14 @@ __device__ __forceinline__ void store_row(T* dst, const float (&o)[V]) {
 // block to arrive joins the unit's parts. A thread takes V columns at a time.
 template <typename T, int V>
 __device__ __forceinline__ void finish_unit(const DecodeArgs& a, const Cursor& c, const Split& sp, SchedSmem* s,
-                                            const float* s_w, const float2* s_wml, int ld, float scale_log2) {
+                                            float* s_w, const float2* s_wml, int ld, float scale_log2) {
   const int G = a.Nq / a.Nkv, D = a.D, per_row = D / V;
   const int hk = c.u / a.groups, g0 = (c.u - hk * a.groups) * a.rows;
   const int n_rows = min(a.rows, G - g0);
   const int64_t row0 = (int64_t)c.b * a.Nq + (int64_t)hk * G + g0;
   const int64_t slot_floats = (int64_t)a.rows * (D + 4);  // o [rows][D], then (m, l) [rows], 16-byte aligned
   const bool whole = c.t_begin == 0 && c.t_end == c.ks.nt;
+  float2* s_join = reinterpret_cast<float2*>(s_w);  // the warps' results are no longer needed there
   float* slot = a.part + (2 * (int64_t)blockIdx.x + (c.t_begin > 0 ? 0 : 1)) * slot_floats;
   auto write = [&](int r, int d, float m, float l, float (&o)[V]) {
     const float inv = l != 0.f ? 1.f / l : 0.f;  // l = 0: no key was seen
@@ -224,60 +227,90 @@ __device__ __forceinline__ void finish_unit(const DecodeArgs& a, const Cursor& c
     }
   }
   if (whole) return;
+  // Part i of the unit is the tail of block c0 (i = 0) or the head of block c0 + i. Up to kJoin parts
+  // are joined by the last block to arrive among them; of more, each kJoin in a row first become one
+  // (in the slot of the first of them), and the last block to finish such a group joins the groups. One
+  // block joining all parts of a long sequence alone took longer than reading its keys.
   const int c0 = sp.owner(c.first), parts = sp.owner(c.first + c.ks.nt - 1) - c0 + 1;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) s->last = atomicInc(a.ctr + c0, (unsigned)parts - 1) == (unsigned)parts - 1;
-  __syncthreads();
-  if (!s->last) return;
-  __threadfence();
-  // part i of the unit: the tail of block c0, then the heads of the blocks behind it
-  const float* p0 = a.part + (2 * (int64_t)c0 + 1) * slot_floats;
-  const float* pi = a.part + 2 * (int64_t)c0 * slot_floats;
-  constexpr int kAhead = 4;  // parts loaded at once
-  for (int x = threadIdx.x; x < n_rows * per_row; x += kThreads) {
-    const int r = x / per_row, d = (x - r * per_row) * V;
-    float m = -INFINITY, l = 0.f, o[V] = {};
-    for (int i0 = 0; i0 < parts; i0 += kAhead) {
-      float2 ml[kAhead];
-      float po[kAhead][V];
+  const int groups = (parts + kJoin - 1) / kJoin;
+  auto part_slot = [&](int i) { return a.part + (2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0)) * slot_floats; };
+  // whether this block is the last of n to arrive at a counter
+  auto last_of = [&](unsigned* ctr, int n) -> bool {
+    if (n == 1) return true;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) s->last = atomicInc(ctr, (unsigned)n - 1) == (unsigned)n - 1;
+    __syncthreads();
+    const bool last = s->last;
+    __threadfence();
+    return last;
+  };
+  // joins n parts i0, i0 + step, ...; the result replaces part i0, or is the unit's
+  auto join = [&](int i0, int n, int step, bool final) {
+    for (int x = threadIdx.x; x < n_rows * per_row; x += kThreads) {
+      const int r = x / per_row, d = (x - r * per_row) * V;
+      float m = -INFINITY, l = 0.f, o[V] = {};
+      constexpr int kAhead = 8;  // parts loaded at once
+      for (int j0 = 0; j0 < n; j0 += kAhead) {
+        float2 ml[kAhead];
+        float po[kAhead][V];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + j;
-        const float* p = i == 0 ? p0 : pi + 2 * (int64_t)i * slot_floats;
-        ml[j] = make_float2(-INFINITY, 0.f);
-        if (i < parts) {
-          ml[j] = __ldcg(reinterpret_cast<const float2*>(p + a.rows * D) + r);
-          if constexpr (V == 4) {
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
-            po[j][0] = t.x; po[j][1] = t.y; po[j][2] = t.z; po[j][3] = t.w;
-          } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k) po[j][k] = __ldcg(p + r * D + d + k);
-          }
-        } else {
+        for (int j = 0; j < kAhead; ++j) {
+          ml[j] = make_float2(-INFINITY, 0.f);
 #pragma unroll
           for (int k = 0; k < V; ++k) po[j][k] = 0.f;
+          if (j0 + j < n) {
+            const float* p = part_slot(i0 + (j0 + j) * step);
+            ml[j] = __ldcg(reinterpret_cast<const float2*>(p + a.rows * D) + r);
+            if constexpr (V == 4) {
+              const float4 t = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
+              po[j][0] = t.x; po[j][1] = t.y; po[j][2] = t.z; po[j][3] = t.w;
+            } else {
+#pragma unroll
+              for (int k = 0; k < V; ++k) po[j][k] = __ldcg(p + r * D + d + k);
+            }
+          }
+        }
+        float mn = m;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) mn = fmaxf(mn, ml[j].x);
+        const float f = shrink(m, mn, scale_log2);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] *= f;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const float g = shrink(ml[j].x, m, scale_log2);
+          l = fmaf(ml[j].y, g, l);
+#pragma unroll
+          for (int k = 0; k < V; ++k) o[k] = fmaf(po[j][k], g, o[k]);
         }
       }
-      float mn = m;
+      if (final) {
+        write(r, d, m, l, o);
+      } else {
+        float* p = part_slot(i0);
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) mn = fmaxf(mn, ml[j].x);
-      const float f = shrink(m, mn, scale_log2);
-      m = mn;
-      l *= f;
-#pragma unroll
-      for (int k = 0; k < V; ++k) o[k] *= f;
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const float g = shrink(ml[j].x, m, scale_log2);
-        l = fmaf(ml[j].y, g, l);
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = fmaf(po[j][k], g, o[k]);
+        for (int k = 0; k < V; ++k) __stcg(p + r * D + d + k, o[k]);
+        s_join[x] = make_float2(m, l);
       }
     }
-    write(r, d, m, l, o);
+    if (!final) {
+      // (m, l) of part i0 is still read above by the other columns of its row
+      __syncthreads();
+      for (int r = threadIdx.x; r < n_rows; r += kThreads)
+        __stcg(reinterpret_cast<float2*>(part_slot(i0) + a.rows * D) + r, s_join[r * per_row]);
+    }
+  };
+  const int i0 = ((int)blockIdx.x - c0) / kJoin * kJoin, n = min(kJoin, parts - i0);
+  if (!last_of(a.ctr + c0 + i0, n)) return;
+  if (groups == 1) {
+    join(0, parts, 1, true);
+    return;
   }
+  if (n > 1) join(i0, n, 1, false);
+  if (last_of(a.ctr + kDecodeMaxCtas + c0, groups)) join(0, groups, kJoin, true);
 }
 
 // Any type, head size up to 32 * DT, any alignment: a warp takes a key at a time, lane = column.
@@ -636,11 +669,23 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) decode_tc_kernel(De
   cp_wait<0>();
 }
 
+// Raises a kernel's limit of dynamic shared memory, once per device.
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (ready.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  return e;
+}
+
 template <typename T, int D, int NB>
 cudaError_t launch_tc(const DecodeArgs& a, cudaStream_t st) {
   using C = TcCfg<D, NB>;
   auto kernel = decode_tc_kernel<T, D, NB>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> ready{0};  // devices whose kernel may use that much shared memory
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, ready);
   if (e != cudaSuccess) return e;
   const int grid = min((NB == 1 ? 2 : 1) * a.num_sms, kDecodeMaxCtas);
   kernel<<<grid, kThreads, C::kSmem, st>>>(a, a.scale * 1.4426950408889634f);
@@ -678,7 +723,7 @@ int decode_rows(int dtype, int Nq, int Nkv, int D) {
 }
 
 int64_t decode_workspace_bytes(int rows, int D) {
-  return 2LL * kDecodeMaxCtas * rows * (D + 4) * (int64_t)sizeof(float) + kDecodeMaxCtas * (int64_t)sizeof(unsigned);
+  return 2LL * kDecodeMaxCtas * rows * (D + 4) * (int64_t)sizeof(float) + 2 * kDecodeMaxCtas * (int64_t)sizeof(unsigned);
 }
 
 cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t st) {

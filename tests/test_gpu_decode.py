@@ -207,7 +207,7 @@ def test_repeats_and_shared_workspace_are_bit_identical():
             for x, y in zip(want, c.run(ws=ws)):
                 assert torch.equal(x, y)
     assert torch.equal(big.run(stats=False)[0], fresh[0][0])
-    assert int(ws[:4 * 512].view(torch.int32).abs().sum()) == 0  # the arrival counters
+    assert int(ws[:4 * 2 * 512].view(torch.int32).abs().sum()) == 0  # the arrival counters
 
 
 def test_graph_replay_with_new_lengths():
