@@ -5,7 +5,7 @@
 // for all query heads that share it, so the call is bound by HBM: 2 * keys * Nkv * D elements.
 //
 // Division of the work: a unit is one sequence's KV head with up to `rows` of its query heads. The
-// units' tiles (of kTile keys) are laid end to end and cut into equal ranges, one per block, so that
+// units' tiles (of kWarps times what a warp works on at once) are laid end to end and cut into equal ranges, one per block, so that
 // one long sequence and many short ones load the GPU alike. Lengths are read on the device (the
 // host never sees them, and the call can be captured into a graph); every block finds its own range
 // by a scan over them. A unit inside one block is finished there. A unit cut between blocks leaves
@@ -27,8 +27,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kWarpKeys = 16;                // keys of a tile that one warp works on
-constexpr int kTile = kWarps * kWarpKeys;    // keys per tile
+constexpr int kGenericKeys = 16;             // keys of a tile that one warp works on, one at a time
 constexpr int kJoin = 16;                    // parts of a unit that one block joins
 constexpr int kGenericRows = 4;              // query heads of a unit outside the tensor-core kernel
 
@@ -57,6 +56,7 @@ struct SchedSmem {
 
 // Finds the sequence that holds this block's first tile. Every sequence has units_b * nt_b tiles.
 // Returns the number of blocks that take part (this block does not if its index is not below it).
+template <int TILE>
 __device__ __forceinline__ int find_range(const DecodeArgs& a, SchedSmem* s, Split* sp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per_seq = a.Nkv * a.groups;
@@ -65,7 +65,7 @@ __device__ __forceinline__ int find_range(const DecodeArgs& a, SchedSmem* s, Spl
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     KeySpan ks;
-    ks.set(row_length(a.p, b, a.status), a.window, a.sinks, kTile);
+    ks.set(row_length(a.p, b, a.status), a.window, a.sinks, TILE);
     mine += (long long)ks.nt * per_seq;
   }
   long long incl = mine;
@@ -90,7 +90,7 @@ __device__ __forceinline__ int find_range(const DecodeArgs& a, SchedSmem* s, Spl
     if (want >= at && want < at + mine) {
       for (int b = b0;; ++b) {
         KeySpan ks;
-        ks.set(row_length(a.p, b, nullptr), a.window, a.sinks, kTile);
+        ks.set(row_length(a.p, b, nullptr), a.window, a.sinks, TILE);
         const long long here = (long long)ks.nt * per_seq;
         if (want < at + here) {
           s->b = b;
@@ -105,7 +105,8 @@ __device__ __forceinline__ int find_range(const DecodeArgs& a, SchedSmem* s, Spl
   return n;
 }
 
-// A walk over the tiles of a block's range, unit by unit.
+// A walk over the tiles (of TILE keys) of a block's range, unit by unit.
+template <int TILE>
 struct Cursor {
   KeySpan ks;
   int b, u;       // sequence, unit within it
@@ -116,7 +117,7 @@ struct Cursor {
 
   __device__ __forceinline__ void open(const DecodeArgs& a, const SchedSmem* s, const Split& sp) {
     b = s->b;
-    ks.set(row_length(a.p, b, nullptr), a.window, a.sinks, kTile);
+    ks.set(row_length(a.p, b, nullptr), a.window, a.sinks, TILE);
     const int64_t begin = sp.begin(blockIdx.x);
     const int64_t off = begin - s->unit_first;
     u = (int)(off / ks.nt);
@@ -133,7 +134,7 @@ struct Cursor {
     if (++u == a.Nkv * a.groups) {
       u = 0;
       ++b;
-      ks.set(row_length(a.p, b, nullptr), a.window, a.sinks, kTile);
+      ks.set(row_length(a.p, b, nullptr), a.window, a.sinks, TILE);
     }
     t = t_begin = 0;
     t_end = (int)min((int64_t)ks.nt, left);
@@ -180,8 +181,8 @@ __device__ __forceinline__ void store_row(T* dst, const float (&o)[V]) {
 // l of the unit's query heads lie in shared memory: s_w [kWarps][rows][ld], s_wml [kWarps][rows] (m, l).
 // They are merged, and written out if the unit is whole; else left in the workspace, where the last
 // block to arrive joins the unit's parts. A thread takes V columns at a time.
-template <typename T, int V>
-__device__ __forceinline__ void finish_unit(const DecodeArgs& a, const Cursor& c, const Split& sp, SchedSmem* s,
+template <typename T, int V, int TILE>
+__device__ __forceinline__ void finish_unit(const DecodeArgs& a, const Cursor<TILE>& c, const Split& sp, SchedSmem* s,
                                             float* s_w, const float2* s_wml, int ld, float scale_log2) {
   const int G = a.Nq / a.Nkv, D = a.D, per_row = D / V;
   const int hk = c.u / a.groups, g0 = (c.u - hk * a.groups) * a.rows;
@@ -322,10 +323,11 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeArgs a, float sc
   float* s_w = smem;                                                    // [kWarps][R][D]
   float2* s_wml = reinterpret_cast<float2*>(s_w + kWarps * R * D);      // [kWarps][R] (kWarps * R is even)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kTile = kWarps * kGenericKeys;
   Split sp;
-  const int n = find_range(a, &sched, &sp);
+  const int n = find_range<kTile>(a, &sched, &sp);
   if ((int)blockIdx.x >= n) return;
-  Cursor c;
+  Cursor<kTile> c;
   c.open(a, &sched, sp);
   const int G = a.Nq / a.Nkv;
   const T* K = static_cast<const T*>(a.k);
@@ -347,8 +349,8 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeArgs a, float sc
       }
     }
     for (; c.t < c.t_end; ++c.t) {
-      const int k0 = c.ks.start(c.t, kTile) + warp * kWarpKeys;
-      for (int j = k0; j < k0 + kWarpKeys; ++j) {
+      const int k0 = c.ks.start(c.t, kTile) + warp * kGenericKeys;
+      for (int j = k0; j < k0 + kGenericKeys; ++j) {
         if (!c.ks.sees(j)) continue;  // a key that is not seen is not read: its page may be anyone's
         const int pi = page_of(a.p, j);
         const int page = __ldg(a.p.page_table + (int64_t)c.b * a.p.max_pages + pi);
@@ -397,18 +399,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeArgs a, float sc
   } while (c.next_unit(a));
 }
 
-// ---- the tensor-core kernel ------------------------------------------------------------------------
-// bf16 or fp16, head size 64 or 128. Each warp works on 16 keys of a tile on its own: it brings them
-// into its ring of shared-memory stages with 16-byte asynchronous copies (kStages - 1 steps ahead, over
-// the ends of units, so that HBM is never waited for between them), and multiplies
-//   S^T [16 keys x 8 NB heads] = K Q^T         (K by ldmatrix, Q held in registers)
-//   O^T [D x 8 NB heads] += V^T P^T            (V by ldmatrix.trans, P^T from S^T by movmatrix)
-// with m16n8k16 products and fp32 sums. Keys are the rows of the first product, so a group of up to
-// 8 query heads costs 8 columns and not 16. The blocks' warps meet only at the end of a unit.
-// P in 16 bits: fp16 keeps 2^-11 of a weight; bf16 would keep 2^-8, so it goes in as two terms, p and
-// what rounding left of it (2^-16): the second product is free, the call waits for HBM.
-// tcgen05 would pad the 1 to 16 rows of queries to 64 or 128 and fill its operands through the same
-// shared memory; at most 16 rows of heads, mma.sync is far from its limit here.
+// ---- streaming keys and values into shared memory ---------------------------------------------------
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -421,6 +412,100 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+
+// A warp's ring of shared-memory stages. A stage holds KEYS keys and as many values, rows of CHUNKS
+// 16-byte chunks, chunk c of row r at place KSwz(r, c) (values: VSwz) of its row, so that the reads of
+// the products fall into different banks. Stages are filled STAGES - 1 steps ahead with asynchronous
+// copies, past the ends of units, so that HBM is never waited for between them. Keys that are not seen
+// are not read: their rows become zeros, and s_seen tells the seen ones.
+template <int KEYS, int CHUNKS, int STAGES, int ES, typename KSwz, typename VSwz>
+struct Feeder {
+  static constexpr int kTile = kWarps * KEYS;
+  static constexpr int kRowBytes = CHUNKS * 16;
+  static constexpr int kHalf = KEYS * kRowBytes;   // bytes of a stage's keys (or values)
+  static constexpr int kRing = STAGES * 2 * kHalf;
+  static constexpr int kRpi = 32 / CHUNKS;         // rows a warp copies per instruction
+  static_assert(32 % CHUNKS == 0 && KEYS % kRpi == 0 && KEYS <= 32, "rows of a copy");
+  Cursor<kTile> p;  // the tile being fetched
+  uint32_t ring;    // shared-memory address of the warp's ring
+  unsigned* seen_bits;  // [STAGES]
+  int key, page, real;  // lane r looks after key r mod KEYS: its page, looked up a step ahead
+  bool seen, more;
+
+  __device__ __forceinline__ void open(const DecodeArgs& a, const Cursor<kTile>& c, uint32_t ring_addr, unsigned* bits,
+                                       int real_chunks) {
+    p = c;
+    ring = ring_addr;
+    seen_bits = bits;
+    real = real_chunks;
+    key = 0;
+    page = -1;
+    more = true;
+    look_up(a);
+    for (int i = 0; i < STAGES - 1; ++i) fetch(a, i);
+  }
+  __device__ __forceinline__ void look_up(const DecodeArgs& a) {
+    key = p.ks.start(p.t, kTile) + (threadIdx.x >> 5) * KEYS + ((threadIdx.x & 31) & (KEYS - 1));
+    seen = p.ks.sees(key);
+    if (seen) page = __ldg(a.p.page_table + (int64_t)p.b * a.p.max_pages + page_of(a.p, key));
+  }
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, int stage) {
+    const int lane = threadIdx.x & 31;
+    if (more) {
+      const bool ok = seen && page >= 0 && page < a.p.num_pages;
+      if (seen && !ok && lane < KEYS) report(a.status, ATTN_ERR_DATA);
+      const int hk = p.u / a.groups;
+      const int64_t off = ok ? page * a.p.page_stride +
+                                   (int64_t)(key - page_of(a.p, key) * a.p.page_size) * a.p.tok_stride + hk * a.p.head_stride
+                             : 0;
+      const unsigned oks = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) seen_bits[stage] = oks;
+      const uint32_t dst = ring + stage * 2 * kHalf;
+      const uint8_t* K = static_cast<const uint8_t*>(a.k);
+      const uint8_t* V = static_cast<const uint8_t*>(a.v);
+#pragma unroll
+      for (int i = 0; i < KEYS / kRpi; ++i) {
+        const int row = i * kRpi + lane / CHUNKS, chunk = lane % CHUNKS;
+        const int64_t at = __shfl_sync(0xffffffffu, off, row) * ES + chunk * 16;
+        const bool v = ((oks >> row) & 1) && chunk < real;
+        const uint32_t to = dst + row * kRowBytes;
+        cp_async16(to + KSwz::at(row, chunk) * 16, K + (v ? at : 0), v);
+        cp_async16(to + kHalf + VSwz::at(row, chunk) * 16, V + (v ? at : 0), v);
+      }
+      if (++p.t == p.t_end) more = p.next_unit(a);
+      if (more) look_up(a);
+    }
+    cp_commit();
+  }
+  // Waits for the stage of the current step and fetches into the one that the last step has left.
+  __device__ __forceinline__ void step(const DecodeArgs& a, int stage) {
+    cp_wait<STAGES - 2>();
+    __syncwarp();
+    fetch(a, stage == 0 ? STAGES - 1 : stage - 1);
+  }
+};
+struct SwzNone {
+  __device__ static __forceinline__ int at(int, int c) { return c; }
+};
+struct SwzRow8 {  // eight rows at one chunk (ldmatrix)
+  __device__ static __forceinline__ int at(int r, int c) { return c ^ (r & 7); }
+};
+struct SwzPair {  // two rows at four chunks in a row
+  __device__ static __forceinline__ int at(int r, int c) { return c ^ ((r & 1) << 2); }
+};
+
+// ---- the tensor-core kernel ------------------------------------------------------------------------
+// bf16 or fp16, head size 64 or 128. Each warp works on 16 MB keys of a tile on its own: it brings them
+// into its ring of shared-memory stages with 16-byte asynchronous copies (kStages - 1 steps ahead, over
+// the ends of units, so that HBM is never waited for between them), and multiplies
+//   S^T [16 MB keys x 8 NB heads] = K Q^T      (K by ldmatrix, Q held in registers)
+//   O^T [D x 8 NB heads] += V^T P^T            (V by ldmatrix.trans, P^T from S^T by movmatrix)
+// with m16n8k16 products and fp32 sums. Keys are the rows of the first product, so a group of up to
+// 8 query heads costs 8 columns and not 16. The blocks' warps meet only at the end of a unit.
+// P in 16 bits: fp16 keeps 2^-11 of a weight; bf16 would keep 2^-8, so it goes in as two terms, p and
+// what rounding left of it (2^-16): the second product is free, the call waits for HBM.
+// tcgen05 would pad the 1 to 16 rows of queries to 64 or 128 and fill its operands through the same
+// shared memory; at most 16 rows of heads, mma.sync is far from its limit here.
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -462,10 +547,16 @@ __device__ __forceinline__ float ex2_approx(float x) {
 
 template <int D, int NB>
 struct TcCfg {
+  // 16-key blocks that a warp works on at once: as many as make 8 KB of keys and values, so that the
+  // fixed cost of a step (the copies' addresses, the maximum's shuffles) is spread alike
+  static constexpr int kMb = 128 / D;
+  static constexpr int kWarpKeys = 16 * kMb;
   static constexpr int kRows = 8 * NB;                       // query heads of a unit
-  static constexpr int kStages = D == 128 ? 3 : 6;           // ring stages of a warp
-  static constexpr int kHalf = kWarpKeys * D * 2;            // bytes of a stage's keys (or values)
-  static constexpr int kRing = kWarps * kStages * 2 * kHalf;
+  static constexpr int kStages = 3;                          // ring stages of a warp
+  using Feed = Feeder<kWarpKeys, D / 8, kStages, 2, SwzRow8, SwzRow8>;
+  static constexpr int kTile = Feed::kTile;
+  static constexpr int kHalf = Feed::kHalf;
+  static constexpr int kRing = kWarps * Feed::kRing;
   static constexpr int kLd = D + 4;                          // padded row of the merge area
   static constexpr int kMerge = kWarps * kRows * kLd * 4;
   static constexpr int kSmem = kRing + kMerge + kWarps * kRows * 8;
@@ -475,65 +566,23 @@ template <typename T, int D, int NB>
 __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) decode_tc_kernel(DecodeArgs a, float scale_log2) {
   using C = TcCfg<D, NB>;
   constexpr bool kF16 = sizeof(T) == 2 && std::is_same<T, __half>::value;
-  constexpr int kCpr = D / 8;        // 16-byte chunks per row
-  constexpr int kRpi = 32 / kCpr;    // rows a warp copies per instruction
-  constexpr int kSteps = kWarpKeys / kRpi;
+  constexpr int kTile = C::kTile, kMb = C::kMb;
   extern __shared__ __align__(128) uint8_t tc_smem[];
   __shared__ SchedSmem sched;
   __shared__ unsigned s_seen[kWarps][C::kStages];  // bit r: key r of the stage is visible
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* ring = tc_smem + warp * C::kStages * 2 * C::kHalf;
   float* s_w = reinterpret_cast<float*>(tc_smem + C::kRing);
   float2* s_wml = reinterpret_cast<float2*>(tc_smem + C::kRing + C::kMerge);
-  const uint32_t ring0 = smem_addr(ring);
+  const uint32_t ring0 = smem_addr(tc_smem + warp * C::Feed::kRing);
 
   Split sp;
-  const int n = find_range(a, &sched, &sp);
+  const int n = find_range<kTile>(a, &sched, &sp);
   if ((int)blockIdx.x >= n) return;
-  Cursor c, p;  // the tile being multiplied, the tile being fetched
+  Cursor<kTile> c;  // the tile being multiplied
   c.open(a, &sched, sp);
-  p = c;
-  bool more = true;
+  typename C::Feed feed;
+  feed.open(a, c, ring0, s_seen[warp], D / 8);
   const int G = a.Nq / a.Nkv;
-  const uint8_t* K = static_cast<const uint8_t*>(a.k);
-  const uint8_t* V = static_cast<const uint8_t*>(a.v);
-
-  // lane r (and r + 16) looks after key r of the warp's 16: its page, looked up a step ahead
-  int key = 0, page = -1;
-  bool seen = false;
-  auto look_up = [&]() {
-    key = p.ks.start(p.t, kTile) + warp * kWarpKeys + (lane & 15);
-    seen = p.ks.sees(key);
-    if (seen) page = __ldg(a.p.page_table + (int64_t)p.b * a.p.max_pages + page_of(a.p, key));
-  };
-  auto fetch = [&](int stage) {
-    if (more) {
-      bool ok = seen && page >= 0 && page < a.p.num_pages;
-      if (seen && !ok && lane < 16) report(a.status, ATTN_ERR_DATA);
-      const int hk = p.u / a.groups;
-      const int64_t off = ok ? page * a.p.page_stride +
-                                   (int64_t)(key - page_of(a.p, key) * a.p.page_size) * a.p.tok_stride + hk * a.p.head_stride
-                             : 0;
-      const unsigned oks = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) s_seen[warp][stage] = oks;
-      const uint32_t dst = ring0 + stage * 2 * C::kHalf;
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int row = i * kRpi + lane / kCpr, chunk = lane % kCpr;
-        const int64_t o = (__shfl_sync(0xffffffffu, off, row) + chunk * 8) * 2;
-        const bool v = (oks >> row) & 1;
-        const uint32_t at = dst + row * (D * 2) + ((chunk ^ (row & 7)) << 4);
-        cp_async16(at, K + (v ? o : 0), v);
-        cp_async16(at + C::kHalf, V + (v ? o : 0), v);
-      }
-      if (++p.t == p.t_end) more = p.next_unit(a);
-      if (more) look_up();
-    }
-    cp_commit();
-  };
-  look_up();
-#pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) fetch(s);
 
   int stage = 0;
   const int g = lane >> 2, t2 = (lane & 3) * 2;
@@ -566,32 +615,39 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) decode_tc_kernel(De
         for (int i = 0; i < 4; ++i) o[b][k][i] = 0.f;
     }
     for (; c.t < c.t_end; ++c.t) {
-      cp_wait<C::kStages - 2>();
-      __syncwarp();  // this step's copies of all lanes are there, and the last step's stage is free
-      fetch(stage == 0 ? C::kStages - 1 : stage - 1);
+      feed.step(a, stage);
       const uint32_t sk = ring0 + stage * 2 * C::kHalf, sv = sk + C::kHalf;
       const unsigned seen_now = s_seen[warp][stage];
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
-      float s[NB][4];
+      float s[NB][kMb][4];
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[b][i] = 0.f;
+        for (int j = 0; j < kMb; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[b][j][i] = 0.f;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        uint32_t kf[4];
-        ldsm4(kf, sk + krow * (D * 2) + (((2 * k + kcol) ^ (krow & 7)) << 4));
 #pragma unroll
-        for (int b = 0; b < NB; ++b) mma16816<kF16>(s[b], kf, q[b][k][0], q[b][k][1]);
+        for (int j = 0; j < kMb; ++j) {
+          uint32_t kf[4];
+          ldsm4(kf, sk + (16 * j + krow) * (D * 2) + (((2 * k + kcol) ^ (krow & 7)) << 4));
+#pragma unroll
+          for (int b = 0; b < NB; ++b) mma16816<kF16>(s[b][j], kf, q[b][k][0], q[b][k][1]);
+        }
       }
-      const bool see0 = (seen_now >> g) & 1, see1 = (seen_now >> (g + 8)) & 1;
-      uint32_t ph[NB][2], pl[NB][2];
+      uint32_t ph[NB][kMb][2], pl[NB][kMb][2];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        if (!see0) s[b][0] = s[b][1] = -INFINITY;
-        if (!see1) s[b][2] = s[b][3] = -INFINITY;
-        // the largest score of each head's 16 keys; the running one only moves where it is exceeded
-        float x0 = fmaxf(s[b][0], s[b][2]), x1 = fmaxf(s[b][1], s[b][3]);
+        // the largest score of each head's keys; the running one only moves where it is exceeded
+        float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kMb; ++j) {
+          if (!((seen_now >> (16 * j + g)) & 1)) s[b][j][0] = s[b][j][1] = -INFINITY;
+          if (!((seen_now >> (16 * j + g + 8)) & 1)) s[b][j][2] = s[b][j][3] = -INFINITY;
+          x0 = fmaxf(x0, fmaxf(s[b][j][0], s[b][j][2]));
+          x1 = fmaxf(x1, fmaxf(s[b][j][1], s[b][j][3]));
+        }
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) {
           x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, i));
@@ -614,31 +670,37 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) decode_tc_kernel(De
         }
         const float c0 = m[b][0] == -INFINITY ? 0.f : -m[b][0] * scale_log2;
         const float c1 = m[b][1] == -INFINITY ? 0.f : -m[b][1] * scale_log2;
-        float e[4];
-        e[0] = ex2_approx(fmaf(s[b][0], scale_log2, c0));
-        e[1] = ex2_approx(fmaf(s[b][1], scale_log2, c1));
-        e[2] = ex2_approx(fmaf(s[b][2], scale_log2, c0));
-        e[3] = ex2_approx(fmaf(s[b][3], scale_log2, c1));
-        l[b][0] += e[0] + e[2];
-        l[b][1] += e[1] + e[3];
-        const uint32_t h0 = pack2<T>(e[0], e[1]), h1 = pack2<T>(e[2], e[3]);
-        ph[b][0] = transpose8(h0);
-        ph[b][1] = transpose8(h1);
-        if constexpr (!kF16) {
-          const float2 r0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h0));
-          const float2 r1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h1));
-          pl[b][0] = transpose8(pack2<T>(e[0] - r0.x, e[1] - r0.y));
-          pl[b][1] = transpose8(pack2<T>(e[2] - r1.x, e[3] - r1.y));
+#pragma unroll
+        for (int j = 0; j < kMb; ++j) {
+          float e[4];
+          e[0] = ex2_approx(fmaf(s[b][j][0], scale_log2, c0));
+          e[1] = ex2_approx(fmaf(s[b][j][1], scale_log2, c1));
+          e[2] = ex2_approx(fmaf(s[b][j][2], scale_log2, c0));
+          e[3] = ex2_approx(fmaf(s[b][j][3], scale_log2, c1));
+          l[b][0] += e[0] + e[2];
+          l[b][1] += e[1] + e[3];
+          const uint32_t h0 = pack2<T>(e[0], e[1]), h1 = pack2<T>(e[2], e[3]);
+          ph[b][j][0] = transpose8(h0);
+          ph[b][j][1] = transpose8(h1);
+          if constexpr (!kF16) {
+            const float2 r0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h0));
+            const float2 r1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h1));
+            pl[b][j][0] = transpose8(pack2<T>(e[0] - r0.x, e[1] - r0.y));
+            pl[b][j][1] = transpose8(pack2<T>(e[2] - r1.x, e[3] - r1.y));
+          }
         }
       }
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        uint32_t vf[4];
-        ldsm4t(vf, sv + vrow * (D * 2) + (((2 * k + vcol) ^ (vrow & 7)) << 4));
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          mma16816<kF16>(o[b][k], vf, ph[b][0], ph[b][1]);
-          if constexpr (!kF16) mma16816<kF16>(o[b][k], vf, pl[b][0], pl[b][1]);
+        for (int j = 0; j < kMb; ++j) {
+          uint32_t vf[4];
+          ldsm4t(vf, sv + (16 * j + vrow) * (D * 2) + (((2 * k + vcol) ^ (vrow & 7)) << 4));
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            mma16816<kF16>(o[b][k], vf, ph[b][j][0], ph[b][j][1]);
+            if constexpr (!kF16) mma16816<kF16>(o[b][k], vf, pl[b][j][0], pl[b][j][1]);
+          }
         }
       }
     }
@@ -669,6 +731,161 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) decode_tc_kernel(De
   cp_wait<0>();
 }
 
+// ---- the fp32 kernel -----------------------------------------------------------------------------
+// float32 with rows of whole 16-byte chunks, head size up to DM. As above a warp streams its keys
+// (8 at a time) through its ring. Scores: four lanes share a key, each multiplies every fourth chunk of
+// the row with all query heads (from shared memory); exchanging halves of the heads, then quarters,
+// leaves lane 4 k + r with the score of key k and head r (R = 8: and r + 4), so that each exponential is
+// computed once. Values: a lane owns a chunk of columns and takes the weights from shared memory. With
+// 4 heads a KV head a key costs about 50 instructions a warp: the call waits for HBM.
+template <int DM, int R>
+struct F32Cfg {
+  static constexpr int kKeys = 8, kStages = 3, kChunks = DM / 4;
+  using Feed = Feeder<kKeys, kChunks, kStages, 4, SwzPair, SwzNone>;
+  static constexpr int kTile = Feed::kTile;
+  static constexpr int kLd = DM;
+  static constexpr int kRing = kWarps * Feed::kRing;
+  static constexpr int kQ = kWarps * R * DM * 4;       // query heads, a copy per warp
+  static constexpr int kP = kWarps * kKeys * R * 4;    // weights
+  static constexpr int kMerge = kWarps * R * kLd * 4;  // over the ring's size: rings stay in flight
+  static constexpr int kSmem = kRing + kQ + kP + kMerge + kWarps * R * 8;
+};
+
+template <int DM, int R>
+__global__ void __launch_bounds__(kThreads) decode_f32_kernel(DecodeArgs a, float scale_log2) {
+  using C = F32Cfg<DM, R>;
+  constexpr int kTile = C::kTile, kKeys = C::kKeys;
+  constexpr int RG = R / 4;            // groups of four heads
+  constexpr int kParts = 32 / C::kChunks;  // keys whose values the lanes take at once (1 or 2)
+  extern __shared__ __align__(128) uint8_t tc_smem[];
+  __shared__ SchedSmem sched;
+  __shared__ unsigned s_seen[kWarps][C::kStages];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint8_t* ring = tc_smem + warp * C::Feed::kRing;
+  float* s_q = reinterpret_cast<float*>(tc_smem + C::kRing) + warp * R * DM;
+  float* s_p = reinterpret_cast<float*>(tc_smem + C::kRing + C::kQ) + warp * kKeys * R;
+  float* s_w = reinterpret_cast<float*>(tc_smem + C::kRing + C::kQ + C::kP);
+  float2* s_wml = reinterpret_cast<float2*>(tc_smem + C::kRing + C::kQ + C::kP + C::kMerge);
+  Split sp;
+  const int n = find_range<kTile>(a, &sched, &sp);
+  if ((int)blockIdx.x >= n) return;
+  Cursor<kTile> c;
+  c.open(a, &sched, sp);
+  typename C::Feed feed;
+  feed.open(a, c, smem_addr(ring), s_seen[warp], a.D / 4);
+  const int G = a.Nq / a.Nkv;
+  int stage = 0;
+  const int kk = lane >> 2, qr = lane & 3;              // key and chunk quarter of the scores
+  const int vk = lane / C::kChunks, vc = lane % C::kChunks;  // key parity and chunk of the values
+  do {
+    const int hk = c.u / a.groups, g0 = (c.u - hk * a.groups) * R;
+    const int n_rows = min(R, G - g0);
+    const float* Q = static_cast<const float*>(a.q) + ((int64_t)c.b * a.Nq + (int64_t)hk * G + g0) * a.D;
+    __syncwarp();
+    for (int x = lane; x < R * DM; x += 32) {
+      const int r = x / DM, d = x % DM;
+      s_q[x] = r < n_rows && d < a.D ? __ldg(Q + r * a.D + d) : 0.f;
+    }
+    __syncwarp();
+    float o[R][4], m[RG], l[RG];
+#pragma unroll
+    for (int r = 0; r < R; ++r) o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
+#pragma unroll
+    for (int i = 0; i < RG; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+    for (; c.t < c.t_end; ++c.t) {
+      feed.step(a, stage);
+      const float4* sk = reinterpret_cast<const float4*>(ring + stage * 2 * C::Feed::kHalf);
+      const float4* sv = sk + kKeys * C::kChunks;
+      const bool see = (s_seen[warp][stage] >> kk) & 1;
+      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+      float s[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < C::kChunks / 4; ++i) {
+        const float4 kv = sk[kk * C::kChunks + SwzPair::at(kk, 4 * i + qr)];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float4 qv = *reinterpret_cast<const float4*>(s_q + r * DM + (4 * i + qr) * 4);
+          s[r] = fmaf(qv.x, kv.x, s[r]);
+          s[r] = fmaf(qv.y, kv.y, s[r]);
+          s[r] = fmaf(qv.z, kv.z, s[r]);
+          s[r] = fmaf(qv.w, kv.w, s[r]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RG; ++i) {
+        // lanes qr and qr ^ 2 exchange two heads each, then qr and qr ^ 1 one: head qr is left
+        const bool hi = qr & 2, odd = qr & 1;
+        const float* t = s + 4 * i;
+        float a0 = hi ? t[2] : t[0], a1 = hi ? t[3] : t[1];
+        a0 += __shfl_xor_sync(0xffffffffu, hi ? t[0] : t[2], 2);
+        a1 += __shfl_xor_sync(0xffffffffu, hi ? t[1] : t[3], 2);
+        float sc = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
+        if (!see) sc = -INFINITY;
+        float x = sc;
+#pragma unroll
+        for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
+        if (__any_sync(0xffffffffu, x > m[i])) {
+          const float mn = fmaxf(m[i], x);
+          const float f = shrink(m[i], mn, scale_log2);
+          m[i] = mn;
+          l[i] *= f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float fr = __shfl_sync(0xffffffffu, f, r);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[4 * i + r][y] *= fr;
+          }
+        }
+        const float e = shrink(sc, m[i], scale_log2);
+        l[i] += e;
+        s_p[kk * R + 4 * i + qr] = e;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kKeys / kParts; ++k) {
+        const int key = k * kParts + vk;
+        const float4 v = sv[key * C::kChunks + vc];
+#pragma unroll
+        for (int i = 0; i < RG; ++i) {
+          const float4 p4 = *reinterpret_cast<const float4*>(s_p + key * R + 4 * i);
+          const float pr[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            o[4 * i + r][0] = fmaf(pr[r], v.x, o[4 * i + r][0]);
+            o[4 * i + r][1] = fmaf(pr[r], v.y, o[4 * i + r][1]);
+            o[4 * i + r][2] = fmaf(pr[r], v.z, o[4 * i + r][2]);
+            o[4 * i + r][3] = fmaf(pr[r], v.w, o[4 * i + r][3]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if constexpr (kParts == 2) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) o[r][y] += __shfl_xor_sync(0xffffffffu, o[r][y], 16);
+      }
+      if (vk == 0)
+        *reinterpret_cast<float4*>(s_w + (warp * R + r) * C::kLd + vc * 4) = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+    }
+#pragma unroll
+    for (int i = 0; i < RG; ++i) {
+#pragma unroll
+      for (int y = 4; y < 32; y <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], y);
+      if (kk == 0) s_wml[warp * R + 4 * i + qr] = make_float2(m[i], l[i]);
+    }
+    __syncthreads();
+    finish_unit<float, 4>(a, c, sp, &sched, s_w, s_wml, C::kLd, scale_log2);
+    __syncthreads();
+  } while (c.next_unit(a));
+  cp_wait<0>();
+}
+
 // Raises a kernel's limit of dynamic shared memory, once per device.
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& ready) {
   int dev = 0;
@@ -689,6 +906,18 @@ cudaError_t launch_tc(const DecodeArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int grid = min((NB == 1 ? 2 : 1) * a.num_sms, kDecodeMaxCtas);
   kernel<<<grid, kThreads, C::kSmem, st>>>(a, a.scale * 1.4426950408889634f);
+  return cudaGetLastError();
+}
+
+template <int DM, int R>
+cudaError_t launch_f32(const DecodeArgs& a, cudaStream_t st) {
+  using C = F32Cfg<DM, R>;
+  auto kernel = decode_f32_kernel<DM, R>;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::kSmem, ready);
+  if (e != cudaSuccess) return e;
+  const int per_sm = 2 * (C::kSmem + 1280) <= 228 * 1024 ? 2 : 1;  // with what the block reserves
+  kernel<<<min(per_sm * a.num_sms, kDecodeMaxCtas), kThreads, C::kSmem, st>>>(a, a.scale * 1.4426950408889634f);
   return cudaGetLastError();
 }
 
@@ -719,7 +948,8 @@ bool tensor_shape(int dtype, int D) { return dtype != ATTN_F32 && (D == 64 || D 
 }  // namespace
 
 int decode_rows(int dtype, int Nq, int Nkv, int D) {
-  return tensor_shape(dtype, D) ? (Nq / Nkv <= 8 ? 8 : 16) : kGenericRows;
+  if (tensor_shape(dtype, D)) return Nq / Nkv <= 8 ? 8 : 16;
+  return dtype == ATTN_F32 && D <= 128 && Nq / Nkv > 4 ? 8 : kGenericRows;
 }
 
 int64_t decode_workspace_bytes(int rows, int D) {
@@ -732,7 +962,11 @@ cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t st) {
                         reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.p.page_stride * 2);
   if (tensor_shape(a.dtype, a.D) && (all & 15u) == 0)
     return a.dtype == ATTN_F16 ? launch_tc_t<__half>(a, st) : launch_tc_t<__nv_bfloat16>(a, st);
-  // the tensor-core kernel's workspace is larger than this one's
+  if (a.dtype == ATTN_F32 && a.D <= 128 && (all & 15u) == 0 && a.D % 4 == 0 && a.p.page_stride % 4 == 0) {
+    if (a.D <= 64) return a.rows == 4 ? launch_f32<64, 4>(a, st) : launch_f32<64, 8>(a, st);
+    return a.rows == 4 ? launch_f32<128, 4>(a, st) : launch_f32<128, 8>(a, st);
+  }
+  // the workspace for the rows of the kernels above is as large as this one's or larger
   a.rows = kGenericRows;
   a.groups = (a.Nq / a.Nkv + a.rows - 1) / a.rows;
   if (a.dtype == ATTN_F32) return launch_t<float>(a, st);

@@ -176,7 +176,7 @@ def test_interleaved_pools(dtype):
         assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("dtype", [BF, F16], ids=IDS)
+@pytest.mark.parametrize("dtype", [BF, F16, F32], ids=IDS)
 def test_unaligned_tensors(dtype):
     """Addresses off the 16-byte boundary take the path without vector loads."""
     c = Case([70, 0, 333], 8, 2, 128, dtype, seed=6)
