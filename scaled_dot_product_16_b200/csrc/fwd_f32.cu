@@ -9,7 +9,15 @@
 // Tiling: a block owns 32 query rows of one (sequence, head); its 4 warps own 8 rows each.
 // Key/value tiles of 32 rows are staged in shared memory; lane = key for the scores and
 // lane = head-dim column for the P.V accumulation. The softmax is the online (streaming)
-// form: the running maximum and sum are rescaled when the maximum grows.
+// form: the running maximum and sum are rescaled when the maximum grows. attn_fwd_sinks leaves out
+// the key tiles between the first keys and the block's window.
+//
+// The tiles come by asynchronous copies (16 bytes at a time where rows allow it), the next one while
+// the current one is multiplied: with plain loads a block of few key tiles spent most of its time
+// waiting for them (2 x 4 x 333 x 80, window 128: 121 us, now 20 us). Rows are padded to whole 16-byte chunks, so that
+// queries and keys are read four columns at a time, and the weights eight rows at a time: the loop is
+// bound by shared-memory reads otherwise. The order of every sum is that of one column, and one key,
+// after the other.
 #include <math.h>
 
 #include "common.cuh"
@@ -22,16 +30,42 @@ constexpr int kBM = 32;       // query rows per block
 constexpr int kBN = 32;       // keys per tile
 constexpr int kWarps = 4;
 constexpr int kRowsPerWarp = kBM / kWarps;
+static_assert(kRowsPerWarp == 8, "the weights of a key are read as two vectors");
+
+// 4 or 16 bytes to shared memory, or zeros where !ok (src is then not read)
+template <int BYTES>
+__device__ __forceinline__ void stage(float* dst, const float* src, bool ok) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(ok ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+
+// kBN rows of D columns into rows of `ld` floats whose columns up to a multiple of 4 become zeros; rows
+// from `rows` on become zeros.
+template <int BYTES>
+__device__ __forceinline__ void stage_tile(float* dst, int ld, const float* src, int64_t stride, int rows, int D) {
+  constexpr int N = BYTES / 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D4 = (D + 3) / 4 * 4;
+  for (int r = warp; r < kBN; r += kWarps)
+    for (int c = lane * N; c < D4; c += 32 * N) {
+      const bool ok = r < rows && c < D;
+      stage<BYTES>(dst + r * ld + c, ok ? src + r * stride + c : src, ok);
+    }
+}
 
 template <int DMAX>
-__global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int tiles_per_seq) {
-  extern __shared__ float smem[];
+__global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int tiles_per_seq, int vec) {
+  extern __shared__ __align__(16) float smem[];
   const int D = a.D, Dv = a.Dv;
-  const int ldk = D + 1;  // padded row of the K tile: lane-strided reads avoid bank conflicts
-  float* sQ = smem;                       // [kBM][D]
-  float* sK = sQ + kBM * D;               // [kBN][D+1]
-  float* sV = sK + kBN * ldk;             // [kBN][Dv]
-  float* sP = sV + kBN * Dv;              // [kWarps][kRowsPerWarp][kBN]
+  const int D4 = (D + 3) / 4 * 4, Dv4 = (Dv + 3) / 4 * 4;
+  const int ldk = (D4 / 4 | 1) * 4;  // row of the K tile, an odd number of chunks: lane-strided 16-byte reads avoid bank conflicts
+  float* sQ = smem;                       // [kBM][D4]
+  float* sP = sQ + kBM * D4;              // [kWarps][kBN][kRowsPerWarp]
+  float* sK = sP + kWarps * kRowsPerWarp * kBN;  // [2][kBN][ldk]
+  float* sV = sK + 2 * kBN * ldk;         // [2][kBN][Dv4]
   __shared__ int s_info[4];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -105,10 +139,19 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
   const int row0 = qt * kBM;
   const int nrows = min(kBM, sq - row0);
   // stage Q (rows past the sequence end are zero-filled)
-  for (int x = threadIdx.x; x < kBM * D; x += blockDim.x) {
-    const int r = x / D, d = x - r * D;
-    sQ[x] = r < nrows ? Q[qoff(row0 + r) + d] : 0.f;
-  }
+  for (int r = warp; r < kBM; r += kWarps)
+    for (int d = lane; d < D4; d += 32) sQ[r * D4 + d] = r < nrows && d < D ? Q[qoff(row0 + r) + d] : 0.f;
+  const int64_t k_stride = a.layout == ATTN_BHSD ? D : (int64_t)a.Nkv * D;
+  const int64_t v_stride = a.layout == ATTN_BHSD ? Dv : (int64_t)a.Nkv * Dv;
+  auto fetch = [&](int j0, int buf) {  // the key tile at j0, or nothing
+    if (vec) {
+      stage_tile<16>(sK + buf * kBN * ldk, ldk, K + kvoff(j0), k_stride, sk - j0, D);
+      stage_tile<16>(sV + buf * kBN * Dv4, Dv4, V + voff(j0), v_stride, sk - j0, Dv);
+    } else {
+      stage_tile<4>(sK + buf * kBN * ldk, ldk, K + kvoff(j0), k_stride, sk - j0, D);
+      stage_tile<4>(sV + buf * kBN * Dv4, Dv4, V + voff(j0), v_stride, sk - j0, Dv);
+    }
+  };
 
   // keys needed by the tile: from the first row's first visible key to the last row's last
   const int kv_end = visible_end(a.mask_mode, row0 + nrows - 1, sq, sk, a.next);
@@ -132,32 +175,38 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
     for (int t = 0; t < DT; ++t) acc[r][t] = 0.f;
   }
 
-  for (int j0 = sink_end > 0 ? 0 : kv_begin; j0 < kv_end; j0 = j0 + kBN == sink_end ? kv_begin : j0 + kBN) {
-    __syncthreads();  // previous tile fully consumed (and Q staged on the first pass)
-    for (int x = threadIdx.x; x < kBN * D; x += blockDim.x) {
-      const int r = x / D, d = x - r * D;
-      const bool in = j0 + r < sk;
-      sK[r * ldk + d] = in ? K[kvoff(j0 + r) + d] : 0.f;
-    }
-    for (int x = threadIdx.x; x < kBN * Dv; x += blockDim.x) {
-      const int r = x / Dv, d = x - r * Dv;
-      sV[x] = j0 + r < sk ? V[voff(j0 + r) + d] : 0.f;
-    }
-    __syncthreads();
+  auto after = [&](int j0) { return j0 + kBN == sink_end ? kv_begin : j0 + kBN; };
+  int buf = 0;
+  const int j_first = sink_end > 0 ? 0 : kv_begin;
+  if (j_first < kv_end) fetch(j_first, 0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  for (int j0 = j_first; j0 < kv_end; j0 = after(j0), buf ^= 1) {
+    if (after(j0) < kv_end) fetch(after(j0), buf ^ 1);  // its last reader passed the barrier below
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();  // this tile is there (and Q, on the first pass)
 
     // scores: lane = key j0 + lane, one value per row of this warp
     float s[kRowsPerWarp];
 #pragma unroll
     for (int r = 0; r < kRowsPerWarp; ++r) s[r] = 0.f;
-    const float* kr = sK + lane * ldk;
-    const float* qr = sQ + warp * kRowsPerWarp * D;
-    for (int d = 0; d < D; ++d) {
-      const float kv = kr[d];
+    const float* kr = sK + buf * kBN * ldk + lane * ldk;
+    const float* qr = sQ + warp * kRowsPerWarp * D4;
+#pragma unroll 4
+    for (int d = 0; d < D4; d += 4) {
+      const float4 kv = *reinterpret_cast<const float4*>(kr + d);
 #pragma unroll
-      for (int r = 0; r < kRowsPerWarp; ++r) s[r] = fmaf(qr[r * D + d], kv, s[r]);
+      for (int r = 0; r < kRowsPerWarp; ++r) {
+        const float4 qv = *reinterpret_cast<const float4*>(qr + r * D4 + d);
+        s[r] = fmaf(qv.x, kv.x, s[r]);
+        s[r] = fmaf(qv.y, kv.y, s[r]);
+        s[r] = fmaf(qv.z, kv.z, s[r]);
+        s[r] = fmaf(qv.w, kv.w, s[r]);
+      }
     }
     const int j = j0 + lane;
     float* pw = sP + warp * kRowsPerWarp * kBN;
+    float pr[kRowsPerWarp];
 #pragma unroll
     for (int r = 0; r < kRowsPerWarp; ++r) {
       const int i = row0 + warp * kRowsPerWarp + r;
@@ -180,23 +229,28 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
       m[r] = mnew;
 #pragma unroll
       for (int t = 0; t < DT; ++t) acc[r][t] *= corr;
-      pw[r * kBN + lane] = p;
+      pr[r] = p;
     }
+    *reinterpret_cast<float4*>(pw + lane * kRowsPerWarp) = make_float4(pr[0], pr[1], pr[2], pr[3]);
+    *reinterpret_cast<float4*>(pw + lane * kRowsPerWarp + 4) = make_float4(pr[4], pr[5], pr[6], pr[7]);
     __syncwarp();
     // P.V: lane owns head-dim columns lane, lane+32, ...
+    const float* vt = sV + buf * kBN * Dv4;
+#pragma unroll 4
     for (int jj = 0; jj < kBN; ++jj) {
-      const float* vr = sV + jj * Dv;
+      const float* vr = vt + jj * Dv4;
       float vv[DT];
 #pragma unroll
       for (int t = 0; t < DT; ++t) vv[t] = (lane + 32 * t) < Dv ? vr[lane + 32 * t] : 0.f;
+      const float4 p0 = *reinterpret_cast<const float4*>(pw + jj * kRowsPerWarp);
+      const float4 p1 = *reinterpret_cast<const float4*>(pw + jj * kRowsPerWarp + 4);
+      const float p[kRowsPerWarp] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
-      for (int r = 0; r < kRowsPerWarp; ++r) {
-        const float p = pw[r * kBN + jj];
+      for (int r = 0; r < kRowsPerWarp; ++r)
 #pragma unroll
-        for (int t = 0; t < DT; ++t) acc[r][t] = fmaf(p, vv[t], acc[r][t]);
-      }
+        for (int t = 0; t < DT; ++t) acc[r][t] = fmaf(p[r], vv[t], acc[r][t]);
     }
-    __syncwarp();
+    __syncthreads();  // this tile is consumed
   }
 
   // ---- epilogue ---------------------------------------------------------------------------
@@ -267,8 +321,8 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
 
 template <int DMAX>
 cudaError_t launch_dmax(const FwdArgs& a, cudaStream_t st) {
-  const size_t smem = sizeof(float) * (size_t)(kBM * a.D + kBN * (a.D + 1) + kBN * a.Dv +
-                                              kWarps * kRowsPerWarp * kBN);
+  const int D4 = (a.D + 3) / 4 * 4, Dv4 = (a.Dv + 3) / 4 * 4;
+  const size_t smem = sizeof(float) * (size_t)(kBM * D4 + kWarps * kRowsPerWarp * kBN + 2 * kBN * ((D4 / 4 | 1) * 4) + 2 * kBN * Dv4);
   cudaError_t e = cudaFuncSetAttribute(fwd_f32_kernel<DMAX>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -282,7 +336,9 @@ cudaError_t launch_dmax(const FwdArgs& a, cudaStream_t st) {
   }
   if (gx <= 0) return cudaSuccess;
   dim3 grid((unsigned)gx, a.Nq);
-  fwd_f32_kernel<DMAX><<<grid, kWarps * 32, smem, st>>>(a, tiles_per_seq);
+  const int vec = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15u) == 0 && a.D % 4 == 0 &&
+                  a.Dv % 4 == 0;
+  fwd_f32_kernel<DMAX><<<grid, kWarps * 32, smem, st>>>(a, tiles_per_seq, vec);
   return cudaGetLastError();
 }
 
