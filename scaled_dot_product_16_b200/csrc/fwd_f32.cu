@@ -6,7 +6,7 @@
 // blog notes that fp32 inputs leave the fast flash path; here fp32 keeps full fp32 FMA
 // arithmetic (no TF32), so the result stays within 1e-5 of the exact value.
 //
-// Tiling: a block owns 32 query rows of one (sequence, head); its 4 warps own 8 rows each.
+// Tiling: a block owns 32 query rows of one (sequence, head); its 8 warps own 4 rows each.
 // Key/value tiles of 32 rows are staged in shared memory; lane = key for the scores and
 // lane = head-dim column for the P.V accumulation. The softmax is the online (streaming)
 // form: the running maximum and sum are rescaled when the maximum grows. attn_fwd_sinks leaves out
@@ -15,7 +15,7 @@
 // The tiles come by asynchronous copies (16 bytes at a time where rows allow it), the next one while
 // the current one is multiplied: with plain loads a block of few key tiles spent most of its time
 // waiting for them (2 x 4 x 333 x 80, window 128: 121 us, now 20 us). Rows are padded to whole 16-byte chunks, so that
-// queries and keys are read four columns at a time, and the weights eight rows at a time: the loop is
+// queries and keys are read four columns at a time, and the weights four rows at a time: the loop is
 // bound by shared-memory reads otherwise. The order of every sum is that of one column, and one key,
 // after the other.
 #include <math.h>
@@ -28,9 +28,8 @@ namespace {
 
 constexpr int kBM = 32;       // query rows per block
 constexpr int kBN = 32;       // keys per tile
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;     // of 4 rows each: 4 warps of 8 rows read K less often but hide less (1.2-1.5 times the time)
 constexpr int kRowsPerWarp = kBM / kWarps;
-static_assert(kRowsPerWarp == 8, "the weights of a key are read as two vectors");
 
 // 4 or 16 bytes to shared memory, or zeros where !ok (src is then not read)
 template <int BYTES>
@@ -206,33 +205,40 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
     }
     const int j = j0 + lane;
     float* pw = sP + warp * kRowsPerWarp * kBN;
-    float pr[kRowsPerWarp];
+    // the rows' reductions side by side, without branches between them
+    float pr[kRowsPerWarp], mx[kRowsPerWarp], ps[kRowsPerWarp], corr[kRowsPerWarp];
+    bool vis[kRowsPerWarp];
 #pragma unroll
     for (int r = 0; r < kRowsPerWarp; ++r) {
-      const int i = row0 + warp * kRowsPerWarp + r;
-      bool vis = (j >= vbeg[r] || (sinks && j < a.sinks)) && j < vend[r];
-      if (vis && mrow0 != nullptr) vis = mrow0[(int64_t)i * a.mask_rs + j] == 0;
-      const float sc = vis ? s[r] * a.scale : -INFINITY;
-      float mx = sc;
+      vis[r] = (j >= vbeg[r] || (sinks && j < a.sinks)) && j < vend[r];
+      if (mrow0 != nullptr && vis[r]) vis[r] = mrow0[(int64_t)(row0 + warp * kRowsPerWarp + r) * a.mask_rs + j] == 0;
+      s[r] = vis[r] ? s[r] * a.scale : -INFINITY;
+      mx[r] = s[r];
+    }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float mnew = fmaxf(m[r], mx);
-      float p = 0.f, corr = 1.f;
-      if (mnew != -INFINITY) {
-        p = vis ? expf(sc - mnew) : 0.f;
-        corr = m[r] == -INFINITY ? 0.f : expf(m[r] - mnew);
-      }
-      float ps = p;
+    for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-      l[r] = l[r] * corr + ps;
+      for (int r = 0; r < kRowsPerWarp; ++r) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], o));
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarp; ++r) {
+      const float mnew = fmaxf(m[r], mx[r]);
+      const float muse = mnew == -INFINITY ? 0.f : mnew;
+      const float e = expf(s[r] - muse), c = expf(m[r] - muse);  // of -inf: 0
+      pr[r] = ps[r] = vis[r] ? e : 0.f;
+      corr[r] = c;
       m[r] = mnew;
 #pragma unroll
-      for (int t = 0; t < DT; ++t) acc[r][t] *= corr;
-      pr[r] = p;
+      for (int t = 0; t < DT; ++t) acc[r][t] *= c;
     }
-    *reinterpret_cast<float4*>(pw + lane * kRowsPerWarp) = make_float4(pr[0], pr[1], pr[2], pr[3]);
-    *reinterpret_cast<float4*>(pw + lane * kRowsPerWarp + 4) = make_float4(pr[4], pr[5], pr[6], pr[7]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < kRowsPerWarp; ++r) ps[r] += __shfl_xor_sync(0xffffffffu, ps[r], o);
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarp; ++r) l[r] = fmaf(l[r], corr[r], ps[r]);
+#pragma unroll
+    for (int r = 0; r < kRowsPerWarp; r += 4)
+      *reinterpret_cast<float4*>(pw + lane * kRowsPerWarp + r) = make_float4(pr[r], pr[r + 1], pr[r + 2], pr[r + 3]);
     __syncwarp();
     // P.V: lane owns head-dim columns lane, lane+32, ...
     const float* vt = sV + buf * kBN * Dv4;
@@ -242,9 +248,10 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
       float vv[DT];
 #pragma unroll
       for (int t = 0; t < DT; ++t) vv[t] = (lane + 32 * t) < Dv ? vr[lane + 32 * t] : 0.f;
-      const float4 p0 = *reinterpret_cast<const float4*>(pw + jj * kRowsPerWarp);
-      const float4 p1 = *reinterpret_cast<const float4*>(pw + jj * kRowsPerWarp + 4);
-      const float p[kRowsPerWarp] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+      float p[kRowsPerWarp];
+#pragma unroll
+      for (int r = 0; r < kRowsPerWarp; r += 4)
+        *reinterpret_cast<float4*>(p + r) = *reinterpret_cast<const float4*>(pw + jj * kRowsPerWarp + r);
 #pragma unroll
       for (int r = 0; r < kRowsPerWarp; ++r)
 #pragma unroll
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
 template <int DMAX>
 cudaError_t launch_dmax(const FwdArgs& a, cudaStream_t st) {
   const int D4 = (a.D + 3) / 4 * 4, Dv4 = (a.Dv + 3) / 4 * 4;
-  const size_t smem = sizeof(float) * (size_t)(kBM * D4 + kWarps * kRowsPerWarp * kBN + 2 * kBN * ((D4 / 4 | 1) * 4) + 2 * kBN * Dv4);
+  const size_t smem = sizeof(float) * (size_t)(kBM * D4 + kBM * kBN + 2 * kBN * ((D4 / 4 | 1) * 4) + 2 * kBN * Dv4);
   cudaError_t e = cudaFuncSetAttribute(fwd_f32_kernel<DMAX>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
