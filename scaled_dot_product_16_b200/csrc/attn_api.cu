@@ -110,7 +110,7 @@ int fwd_impl(const void* q, const void* k, const void* v, const int32_t* cu_seql
   if (dtype != ATTN_BF16 && dtype != ATTN_F32 && dtype != ATTN_F16) return ATTN_ERR_INVALID;
   const int max_mode = x.allow_band ? ATTN_MASK_BAND : ATTN_MASK_CAUSAL_BOTTOMRIGHT;
   if (mask_mode < ATTN_MASK_NONE || mask_mode > max_mode) return ATTN_ERR_INVALID;
-  if (mask_mode == ATTN_MASK_BAND && clamp30(x.pre) + clamp30(x.next) < 0) return ATTN_ERR_INVALID;
+  if (mask_mode == ATTN_MASK_BAND && (int64_t)clamp30(x.pre) + clamp30(x.next) < 0) return ATTN_ERR_INVALID;
   const int Dv = x.Dv < 0 ? D : x.Dv;
   if (Dv < 1 || Dv > D) return ATTN_ERR_INVALID;
   if (x.mask != nullptr && (x.mask_bs < 0 || x.mask_rs < 0)) return ATTN_ERR_INVALID;

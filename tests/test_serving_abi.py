@@ -46,6 +46,14 @@ def test_sinks(lib):
     assert f(B=0) == OK and f(Sq=0, window=1 << 62, sinks=1 << 62) == OK
 
 
+def test_a_band_without_limits_is_not_empty(lib):
+    """Both limits of a band at 2^30 or more are unbounded; their sum does not wrap round."""
+    for pre, nxt in ((1 << 30, 1 << 30), (1 << 40, 1 << 30), ((1 << 63) - 1, (1 << 63) - 1)):
+        rc = lib.attn_fwd_masked(16, 16, 16, None, None, 0, 8, 8, 2, 1, 64, 64, 0.125, 3, pre, nxt, None, 0, 0, 1, 0, 16,
+                                 None, None, None)
+        assert rc == OK, (pre, nxt)
+
+
 def test_decode(lib):
     n = ctypes.c_int64(0)
     ref = ctypes.byref(n)
