@@ -16,6 +16,7 @@ namespace {
 // A warp writes one token's key and value rows (all heads), in vectors of type V. Bound by HBM for
 // whole prompts (each new element is read and written once), by latency for one token per row.
 constexpr int kAppendWarps = 4;
+constexpr int kAppendVecs = 4;  // vectors a lane holds of each of k and v
 
 template <typename V>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a, int vec_per_head) {
@@ -34,6 +35,19 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a,
   V* vc = static_cast<V*>(a.v);
   const int per_row = a.Nkv * vec_per_head;
   for (int t = blockIdx.x * kAppendWarps + (threadIdx.x >> 5); t < a.T; t += n_warps) {
+    // the first vectors of the token are on their way while its place is looked up
+    const V* ks = kn + (int64_t)t * per_row;
+    const V* vs = vn + (int64_t)t * per_row;
+    V rk[kAppendVecs], rv[kAppendVecs];
+    auto load = [&](int x0) {
+#pragma unroll
+      for (int i = 0; i < kAppendVecs; ++i)
+        if (x0 + 32 * i < per_row) {
+          rk[i] = ks[x0 + 32 * i];
+          rv[i] = vs[x0 + 32 * i];
+        }
+    };
+    load(lane);
     int b = t, left = 1;  // row of token t; tokens of the row from t on
     if (a.cu != nullptr) {
       int lo = 0, hi = a.p.B;  // first row whose end lies behind t
@@ -59,12 +73,18 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a,
     }
     // strides in vectors here
     const int64_t at = page * a.p.page_stride + ((int)pos - pi * a.p.page_size) * a.p.tok_stride;
-    const int64_t from = (int64_t)t * per_row;
-    for (int x = lane; x < per_row; x += 32) {
-      const int h = x / vec_per_head;
-      const int64_t to = at + h * a.p.head_stride + (x - h * vec_per_head);
-      kc[to] = kn[from + x];
-      vc[to] = vn[from + x];
+    for (int x0 = lane; x0 < per_row; x0 += 32 * kAppendVecs) {
+      if (x0 != lane) load(x0);
+#pragma unroll
+      for (int i = 0; i < kAppendVecs; ++i) {
+        const int x = x0 + 32 * i;
+        if (x < per_row) {
+          const int h = x / vec_per_head;
+          const int64_t to = at + h * a.p.head_stride + (x - h * vec_per_head);
+          kc[to] = rk[i];
+          vc[to] = rv[i];
+        }
+      }
     }
   }
 }
@@ -83,7 +103,7 @@ cudaError_t launch_append(AppendArgs a, int es, cudaStream_t st) {
 // ---- attn_cache_copy -----------------------------------------------------------------------------
 // Each block takes (pair, chunk) items in turn; bound by HBM (a page's bytes read and written once).
 constexpr int kCopyThreads = 256;
-constexpr int kCopyVecs = 4;  // vectors a thread holds at once
+constexpr int kCopyVecs = 4;  // vectors a thread holds of each of k and v
 
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(PageCopyArgs a, int64_t page_vecs, int64_t stride_vecs,
@@ -98,19 +118,23 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(PageCopyArgs a, int6
       if (threadIdx.x == 0) report(a.status, ATTN_ERR_DATA);
       continue;
     }
+    const V* ks = static_cast<const V*>(a.k) + sd.x * stride_vecs;
+    const V* vs = static_cast<const V*>(a.v) + sd.x * stride_vecs;
+    V* kd = static_cast<V*>(a.k) + sd.y * stride_vecs;
+    V* vd = static_cast<V*>(a.v) + sd.y * stride_vecs;
+    V rk[kCopyVecs], rv[kCopyVecs];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      V* base = static_cast<V*>(kv == 0 ? a.k : a.v);
-      const V* src = base + sd.x * stride_vecs;
-      V* dst = base + sd.y * stride_vecs;
-      V r[kCopyVecs];
+    for (int i = 0; i < kCopyVecs; ++i)
+      if (v0 + i * kCopyThreads < page_vecs) {
+        rk[i] = ks[v0 + i * kCopyThreads];
+        rv[i] = vs[v0 + i * kCopyThreads];
+      }
 #pragma unroll
-      for (int i = 0; i < kCopyVecs; ++i)
-        if (v0 + i * kCopyThreads < page_vecs) r[i] = src[v0 + i * kCopyThreads];
-#pragma unroll
-      for (int i = 0; i < kCopyVecs; ++i)
-        if (v0 + i * kCopyThreads < page_vecs) dst[v0 + i * kCopyThreads] = r[i];
-    }
+    for (int i = 0; i < kCopyVecs; ++i)
+      if (v0 + i * kCopyThreads < page_vecs) {
+        kd[v0 + i * kCopyThreads] = rk[i];
+        vd[v0 + i * kCopyThreads] = rv[i];
+      }
   }
 }
 
@@ -130,7 +154,7 @@ cudaError_t launch_copy(const PageCopyArgs& a, cudaStream_t st) {
 // (children of the row - 1) for each row that holds it. A block owns a range of columns: it reads
 // them for all rows before it writes them, so the new table may be the old one.
 constexpr int kForkThreads = 256;
-constexpr int kForkEntries = 8192;  // staged entries per block
+constexpr int kForkEntries = 1024;  // staged entries per block, where a column has no more
 
 __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkArgs a, int cols) {
   extern __shared__ int32_t sm[];
@@ -194,11 +218,10 @@ constexpr int kOwned = -(1 << 30);  // below: the keeper's slot; kOwned and abov
 struct ResSmem {
   int warp[kResWarps];
   int bad;
-  int taken;   // free pages found so far
   int free_page[kResThreads];
 };
 
-// Exclusive prefix sum over the block; *total gets the sum. Ends with a barrier before reuse of w.
+// Exclusive prefix sum over the block; *total gets the sum. w [kResWarps] may be used again at once.
 __device__ __forceinline__ int block_scan(int v, int* w, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = v;
@@ -207,26 +230,37 @@ __device__ __forceinline__ int block_scan(int v, int* w, int* total) {
     const int t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
+  __syncthreads();  // the last scan's sums have been read
   if (lane == 31) w[warp] = incl;
   __syncthreads();
-  int before = 0, sum = 0;
-  for (int i = 0; i < kResWarps; ++i) {
-    if (i < warp) before += w[i];
-    sum += w[i];
+  int sums = w[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += t;
   }
-  __syncthreads();
-  *total = sum;
-  return before + incl - v;
+  *total = __shfl_sync(0xffffffffu, sums, 31);
+  const int before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : 0) + incl - v;
+}
+
+// kScan counts in a row per thread (beyond n: fill).
+constexpr int kScan = 8;
+__device__ __forceinline__ void load_counts(const int32_t* ref, int p, int n, int fill, int (&r)[kScan]) {
+  if (p + kScan <= n && (reinterpret_cast<uintptr_t>(ref) & 15u) == 0) {  // p is a multiple of kScan
+#pragma unroll
+    for (int i = 0; i < kScan; i += 4) *reinterpret_cast<int4*>(r + i) = *reinterpret_cast<const int4*>(ref + p + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) r[i] = p + i < n ? ref[p + i] : fill;
+  }
 }
 
 __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
   __shared__ ResSmem s;
   extern __shared__ int32_t prefix[];  // [B] first slot of each row
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    s.bad = 0;
-    s.taken = 0;
-  }
+  if (tid == 0) s.bad = 0;
   __syncthreads();
   auto span = [&](int b, int* start, int* i0) -> int {  // slots of row b
     const int len = a.lens[b], add = a.new_tokens != nullptr ? a.new_tokens[b] : 1;
@@ -256,7 +290,14 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
     if (tid == 0) report(a.status, ATTN_ERR_DATA);
     return;
   }
-  auto entry = [&](int slot, int* b, int* i) -> int32_t* {  // table entry of a slot
+  // A slot: its row and table entry, and whether an earlier token of the row lies in its page. Each
+  // thread keeps its first one (with one token per row there is no other).
+  struct Slot {
+    int b;
+    bool partial;
+    int32_t* e;
+  };
+  auto find = [&](int slot) -> Slot {
     int lo = 0, hi = a.B;  // the last row that begins at or before the slot
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -265,14 +306,15 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
     }
     int start = 0, i0 = 0;
     span(lo, &start, &i0);
-    *b = lo;
-    *i = i0 + slot - prefix[lo];
-    return a.table + (int64_t)lo * a.max_pages + *i;
+    const int i = i0 + slot - prefix[lo];
+    return {lo, i == i0 && start != i0 * a.page_size, a.table + (int64_t)lo * a.max_pages + i};
   };
-  int b, i;
+  Slot mine{0, false, nullptr};
+  if (tid < slots) mine = find(tid);
+  auto slot_at = [&](int x) -> Slot { return x == tid ? mine : find(x); };
   // 1: every slot of a shared page asks for it
   for (int x = tid; x < slots; x += kResThreads) {
-    const int page = *entry(x, &b, &i);
+    const int page = *slot_at(x).e;
     if (page >= a.num_pages) s.bad = 1;
     else if (page >= 0 && a.ref[page] != 1) {
       // a page that is held has a count; 0 here would be handed out a second time
@@ -283,7 +325,7 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
   __syncthreads();
   // 2: where all holders ask, the first slot owns the page
   for (int x = tid; x < slots; x += kResThreads) {
-    const int page = *entry(x, &b, &i);
+    const int page = *slot_at(x).e;
     if (page < 0 || page >= a.num_pages) continue;
     const int v = *(volatile int32_t*)(a.ref + page);
     if (v >= 0) continue;
@@ -292,38 +334,46 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
     else if (v + k * kAsk < k) s.bad = 1;  // more rows hold the page than its count says
   }
   __syncthreads();
-  // 3: how many pages are needed, and whether that many are free
+  auto needs = [&](int x, int page) -> bool {  // slot x needs a free page
+    if (page < 0) return true;
+    if (page >= a.num_pages) return false;
+    const int v = a.ref[page];
+    return v < 0 && v != INT32_MIN + x;
+  };
+  // 3: how many pages are needed, and whether that many are free. The first kResThreads of them are
+  // listed on the way.
   int needed = 0;
   for (int x0 = 0; x0 < slots; x0 += kResThreads) {
     const int x = x0 + tid;
-    int need = 0, sum;
-    if (x < slots) {
-      const int page = *entry(x, &b, &i);
-      if (page < 0) need = 1;
-      else if (page < a.num_pages) {
-        const int v = a.ref[page];
-        need = v < 0 && v != INT32_MIN + x;
-      }
-    }
-    block_scan(need, s.warp, &sum);
+    int sum;
+    block_scan(x < slots && needs(x, *slot_at(x).e), s.warp, &sum);
     needed += sum;
   }
   int have = 0;
-  for (int p0 = 0; p0 < a.num_pages && have < needed; p0 += kResThreads) {
-    int sum;
-    block_scan(p0 + tid < a.num_pages && a.ref[p0 + tid] == 0, s.warp, &sum);
+  for (int p0 = 0; p0 < a.num_pages && have < needed; p0 += kResThreads * kScan) {
+    int r[kScan], n = 0, sum;
+    load_counts(a.ref, p0 + tid * kScan, a.num_pages, 1, r);
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) n += r[i] == 0;
+    int at = have + block_scan(n, s.warp, &sum);
+#pragma unroll
+    for (int i = 0; i < kScan; ++i)
+      if (r[i] == 0) {
+        if (at < kResThreads) s.free_page[at] = p0 + tid * kScan + i;
+        ++at;
+      }
     have += sum;
   }
   __syncthreads();
   if (s.bad || have < needed) {
     // undo: an owned page's count is the number of slots that ask for it
     for (int x = tid; x < slots; x += kResThreads) {
-      const int page = *entry(x, &b, &i);
+      const int page = *slot_at(x).e;
       if (page >= 0 && page < a.num_pages && a.ref[page] == INT32_MIN + x) a.ref[page] = INT32_MIN;
     }
     __syncthreads();
     for (int x = tid; x < slots; x += kResThreads) {
-      const int page = *entry(x, &b, &i);
+      const int page = *slot_at(x).e;
       if (page < 0 || page >= a.num_pages) continue;
       const int v = *(volatile int32_t*)(a.ref + page);
       if (v < kOwned) atomicAdd(a.ref + page, 1);
@@ -331,115 +381,165 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
     }
     __syncthreads();
     for (int x = tid; x < slots; x += kResThreads) {
-      const int page = *entry(x, &b, &i);
+      const int page = *slot_at(x).e;
       if (page >= 0 && page < a.num_pages && a.ref[page] < kOwned) atomicAnd(a.ref + page, INT32_MAX);
     }
     if (tid == 0) report(a.status, s.bad ? ATTN_ERR_DATA : ATTN_ERR_PAGES);
     return;
   }
   // 4: hand out the pages, kResThreads slots at a time
-  int p0 = 0;  // pages below it have been looked at
+  int given = 0;              // pages handed out
+  int listed = 0;             // s.free_page holds free pages listed .. listed + kResThreads - 1
   for (int x0 = 0; x0 < slots; x0 += kResThreads) {
     const int x = x0 + tid;
-    int need = 0, v = 0, page = -1, sum;
-    int32_t* e = nullptr;
+    Slot t = mine;
+    int page = -1, sum;
+    bool need = false;
     if (x < slots) {
-      e = entry(x, &b, &i);
-      page = *e;
-      if (page >= 0) v = a.ref[page];
-      need = page < 0 || (v < 0 && v != INT32_MIN + x);
+      t = slot_at(x);
+      page = *t.e;
+      need = needs(x, page);
     }
-    const int rank = block_scan(need, s.warp, &sum);
-    // the next `sum` free pages, in order; a page found but not needed here is found again
-    int found = 0;
-    while (found < sum && p0 < a.num_pages) {
-      const bool is_free = p0 + tid < a.num_pages && a.ref[p0 + tid] == 0;
-      int n;
-      const int at = found + block_scan(is_free, s.warp, &n);
-      if (is_free && at < sum) {
-        s.free_page[at] = p0 + tid;
-        a.ref[p0 + tid] = 1;
+    const int rank = given + block_scan(need, s.warp, &sum);
+    if (given + sum > listed + kResThreads) {
+      // list free pages given .. given + kResThreads - 1: those handed out so far are no longer free
+      int found = given;
+      for (int p0 = 0; p0 < a.num_pages && found < given + sum; p0 += kResThreads * kScan) {
+        int r[kScan], n = 0, more;
+        load_counts(a.ref, p0 + tid * kScan, a.num_pages, 1, r);
+#pragma unroll
+        for (int i = 0; i < kScan; ++i) n += r[i] == 0;
+        int at = found - given + block_scan(n, s.warp, &more);
+#pragma unroll
+        for (int i = 0; i < kScan; ++i)
+          if (r[i] == 0) {
+            if (at < kResThreads) s.free_page[at] = p0 + tid * kScan + i;
+            ++at;
+          }
+        found += more;
       }
-      found += n;
-      if (found <= sum) p0 += kResThreads;
+      listed = given;
       __syncthreads();
     }
-    __syncthreads();
     if (need) {
-      const int to = s.free_page[rank];
-      *e = to;
+      const int to = s.free_page[rank - listed];
+      *t.e = to;
+      a.ref[to] = 1;
       if (page >= 0) {
-        if (v >= kOwned) atomicAdd(a.ref + page, kAsk - 1);
-        int start = 0, i0 = 0;
-        span(b, &start, &i0);
-        // only the first page of a row's slots can hold earlier tokens
-        if (i == i0 && start % a.page_size != 0) {
-          a.copies[2 * b] = page;
-          a.copies[2 * b + 1] = to;
+        // the count of an owned page is its owner's to set
+        if (a.ref[page] >= kOwned) atomicAdd(a.ref + page, kAsk - 1);
+        if (t.partial) {
+          a.copies[2 * t.b] = page;
+          a.copies[2 * t.b + 1] = to;
         }
       }
     }
+    given += sum;
     __syncthreads();
   }
   // 5: a kept page has one holder
   for (int x = tid; x < slots; x += kResThreads) {
-    const int page = *entry(x, &b, &i);
+    const int page = *slot_at(x).e;
     if (a.ref[page] == INT32_MIN + x) a.ref[page] = 1;
   }
 }
 
 // ---- attn_cache_compact --------------------------------------------------------------------------
 // One block scans the counts: with n live pages, the k-th live page at or above n moves to the k-th
-// free page below n. A second kernel renames the pages in the table.
-__global__ void __launch_bounds__(kResThreads) compact_kernel(CompactArgs a) {
+// free page below n. It renames the pages of a small table too; a second kernel, of more blocks, those of
+// a larger one. The call is bound by the latency of that chain (8,192 pages, 4,928 entries: 10 us).
+constexpr int kHoles = 8192;             // holes listed in shared memory; further ones are looked up in copies
+constexpr int64_t kRenameHere = 32768;   // table entries that the one block renames itself
+
+__device__ __forceinline__ int renamed(const CompactArgs& a, int page) {
+  int to = -1;
+  if (page >= 0) {
+    if (page < a.num_pages) to = *(volatile int32_t*)(a.page_map + page);
+    if (to < 0) report(a.status, ATTN_ERR_DATA);  // a page outside the pool, or one without a count
+  }
+  return to;
+}
+
+__global__ void __launch_bounds__(kResThreads) compact_kernel(CompactArgs a, int64_t entries) {
   __shared__ int w[kResWarps];
-  const int tid = threadIdx.x;
+  __shared__ int hole_page[kHoles];
+  // a warp looks at kScan * 32 pages in a row, 32 at a time, so that its accesses are whole lines; ranks
+  // come from ballots
+  constexpr int kStep = kResThreads * kScan;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int p_warp = (tid >> 5) * (kScan * 32) + lane;
+  const unsigned below = (1u << lane) - 1u;
   const int pairs = a.num_pages / 2;
-  int live = 0;
-  for (int p0 = 0; p0 < a.num_pages; p0 += kResThreads) {
-    int sum;
-    block_scan(p0 + tid < a.num_pages && a.ref[p0 + tid] > 0, w, &sum);
+  int live = 0, r[kScan];
+  auto load = [&](int p0) {
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) {
+      const int p = p0 + p_warp + 32 * i;
+      r[i] = p < a.num_pages ? a.ref[p] : 0;
+    }
+  };
+  for (int p0 = 0; p0 < a.num_pages; p0 += kStep) {
+    int n = 0, sum;
+    load(p0);
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) n += r[i] > 0;
+    block_scan(n, w, &sum);
     live += sum;
   }
   int holes = 0, moved = 0;
-  for (int p0 = 0; p0 < a.num_pages; p0 += kResThreads) {
-    const int p = p0 + tid;
-    const int ref = p < a.num_pages ? a.ref[p] : 0;
-    const bool hole = p < live && ref <= 0, high = p >= live && ref > 0;
-    int nh, nm;
-    const int h = holes + block_scan(hole, w, &nh);
-    const int m = moved + block_scan(high, w, &nm);
-    if (hole) a.copies[2 * h + 1] = p;
-    __syncthreads();  // the holes of these pages are listed before their movers look them up
-    if (p < a.num_pages) {
-      if (high) {
-        const int to = *(volatile int32_t*)(a.copies + 2 * m + 1);
-        a.copies[2 * m] = p;
-        a.page_map[p] = to;
-        a.ref_out[to] = ref;
-        a.ref_out[p] = 0;
-      } else {
-        a.page_map[p] = ref > 0 ? p : -1;
-        if (!hole) a.ref_out[p] = ref > 0 ? ref : 0;  // a hole's count is its mover's
-      }
+  for (int p0 = 0; p0 < a.num_pages; p0 += kStep) {
+    if (a.num_pages > kStep) load(p0);  // else still there
+    // holes below n and live pages from n on, counted in the halves of a word (at most kStep each)
+    unsigned is_hole[kScan], is_high[kScan];
+    int n = 0, sum;
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) {
+      const int p = p0 + p_warp + 32 * i;
+      is_hole[i] = __ballot_sync(0xffffffffu, p < live && r[i] <= 0);
+      is_high[i] = __ballot_sync(0xffffffffu, p >= live && r[i] > 0);
+      n += __popc(is_hole[i]) + (__popc(is_high[i]) << 16);
     }
-    holes += nh;
-    moved += nm;
+    const int before = block_scan(lane == 31 ? n : 0, w, &sum);  // of the warps before, except in lane 31
+    const int base = __shfl_sync(0xffffffffu, before, 0);
+    int h = holes + (base & 0xffff), m = moved + (base >> 16);
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) {
+      if (is_hole[i] >> lane & 1) {
+        const int at = h + __popc(is_hole[i] & below);
+        if (at < kHoles) hole_page[at] = p0 + p_warp + 32 * i;
+        a.copies[2 * at + 1] = p0 + p_warp + 32 * i;
+      }
+      h += __popc(is_hole[i]);
+    }
+    __syncthreads();  // the holes of these pages are listed before their movers look them up
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) {
+      const int p = p0 + p_warp + 32 * i;
+      if (is_high[i] >> lane & 1) {
+        const int at = m + __popc(is_high[i] & below);
+        const int to = at < kHoles ? hole_page[at] : *(volatile int32_t*)(a.copies + 2 * at + 1);
+        a.copies[2 * at] = p;
+        a.page_map[p] = to;
+        a.ref_out[to] = r[i];
+        a.ref_out[p] = 0;
+      } else if (p < a.num_pages) {
+        a.page_map[p] = r[i] > 0 ? p : -1;
+        if (p >= live) a.ref_out[p] = 0;
+        else if (r[i] > 0) a.ref_out[p] = r[i];  // a hole's count is its mover's
+      }
+      m += __popc(is_high[i]);
+    }
+    holes += sum & 0xffff;
+    moved += sum >> 16;
   }
   for (int x = moved + tid; x < pairs; x += kResThreads) a.copies[2 * x] = a.copies[2 * x + 1] = -1;
   if (tid == 0) *a.live = live;
+  __syncthreads();  // the map is complete
+  for (int64_t x = tid; x < entries; x += kResThreads) a.table_out[x] = renamed(a, a.table[x]);
 }
 
 __global__ void __launch_bounds__(256) rename_kernel(CompactArgs a, int64_t n) {
-  for (int64_t x = blockIdx.x * 256LL + threadIdx.x; x < n; x += gridDim.x * 256LL) {
-    const int page = a.table[x];
-    int to = -1;
-    if (page >= 0) {
-      if (page < a.num_pages) to = a.page_map[page];
-      if (to < 0) report(a.status, ATTN_ERR_DATA);  // a page outside the pool, or one without a count
-    }
-    a.table_out[x] = to;
-  }
+  for (int64_t x = blockIdx.x * 256LL + threadIdx.x; x < n; x += gridDim.x * 256LL) a.table_out[x] = renamed(a, a.table[x]);
 }
 
 }  // namespace
@@ -482,10 +582,10 @@ cudaError_t launch_cache_reserve(const ReserveArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {
-  compact_kernel<<<1, kResThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
   const int64_t n = (int64_t)a.rows * a.max_pages;
-  if (e != cudaSuccess || n == 0) return e;
+  compact_kernel<<<1, kResThreads, 0, st>>>(a, n <= kRenameHere ? n : 0);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || n <= kRenameHere) return e;
   const int64_t blocks = (n + 255) / 256;
   rename_kernel<<<(unsigned)(blocks < 1024 ? blocks : 1024), 256, 0, st>>>(a, n);
   return cudaGetLastError();

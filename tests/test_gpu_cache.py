@@ -227,7 +227,8 @@ def test_reserve_bad_data_changes_nothing():
 
 # ---- compact and copy ------------------------------------------------------------------------------
 @pytest.mark.parametrize("in_place", [False, True])
-@pytest.mark.parametrize("num,p_live", [(1, 1.0), (1, 0.0), (2, 0.5), (1023, 0.3), (1024, 0.6), (5000, 0.9), (4097, 0.02)])
+@pytest.mark.parametrize("num,p_live", [(1, 1.0), (1, 0.0), (2, 0.5), (1023, 0.3), (1024, 0.6), (5000, 0.9), (4097, 0.02), (40000, 0.5),
+                                        (70000, 0.7)])
 def test_compact(num, p_live, in_place):
     rng = np.random.default_rng(num)
     ref = [int(x) for x in (rng.random(num) < p_live) * rng.integers(1, 4, num)]
