@@ -2,9 +2,9 @@
 FMA pipe instead of the MUFU unit.
 
 Method: Cody-Waite style range reduction, 2^x = 2^j * 2^f with j = round(x) and f = x - j in
-[-1/2, 1/2], and a degree-3 polynomial for 2^f whose maximum RELATIVE error on [-1/2, 1/2] is
-minimised by the Remez exchange algorithm (equioscillation on 5 points). Run this script to
-reproduce the coefficients printed into fwd_bf16_sm100.cu:
+[-1/2, 1/2], and a degree-3 (for attn_fwd_sinks degree-5) polynomial for 2^f whose maximum RELATIVE
+error on [-1/2, 1/2] is minimised by the Remez exchange algorithm (equioscillation on 5, or 7,
+points). Run this script to reproduce the coefficients printed into fwd_bf16_sm100.cu:
 
     python scaled_dot_product_16_b200/csrc/fit_exp2_poly.py
 """
@@ -41,15 +41,16 @@ def remez(deg=DEG, iters=30):
 
 
 if __name__ == "__main__":
-    c, e = remez()
-    c32 = c.astype(np.float32)
-    grid = np.linspace(LO, HI, 200001).astype(np.float32)
-    # Horner in float32 as the kernel evaluates it
-    p = np.float32(c32[3])
-    p = p * grid + c32[2]
-    p = p * grid + c32[1]
-    p = p * grid + c32[0]
-    e32 = float(np.max(np.abs(p.astype(np.float64) / 2.0 ** grid.astype(np.float64) - 1)))
-    for i, ci in enumerate(c32):
-        print(f"c{i} = {float(ci):.9e}f")
-    print(f"max relative error: {e:.3e} (exact arithmetic), {e32:.3e} (float32 Horner)")
+    for deg in (DEG, 5):
+        c, e = remez(deg)
+        c32 = c.astype(np.float32)
+        grid = np.linspace(LO, HI, 200001).astype(np.float32)
+        # Horner in float32 as the kernel evaluates it
+        p = np.float32(c32[deg])
+        for ci in c32[deg - 1::-1]:
+            p = p * grid + ci
+        e32 = float(np.max(np.abs(p.astype(np.float64) / 2.0 ** grid.astype(np.float64) - 1)))
+        print(f"degree {deg}")
+        for i, ci in enumerate(c32):
+            print(f"c{i} = {float(ci):.9e}f")
+        print(f"max relative error: {e:.3e} (exact arithmetic), {e32:.3e} (float32 Horner)")

@@ -111,6 +111,27 @@ __device__ __forceinline__ void exp2_poly2(float x0, float x1, float& p0, float&
   p1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
 }
 
+// The same with a polynomial of degree 5 (maximum relative error 7.5e-08), for a pass whose sums are
+// to hold more than 16 bits.
+__device__ __forceinline__ void exp2_poly5(float x0, float x1, float& p0, float& p1) {
+  constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
+  constexpr float a0 = 1.000000119e+00f, a1 = 6.931469440e-01f, a2 = 2.402212024e-01f,
+                  a3 = 5.550713092e-02f, a4 = 9.675540961e-03f, a5 = 1.327647245e-03f;
+  x0 = fmaxf(x0, -126.f);
+  x1 = fmaxf(x1, -126.f);
+  float t0, t1, j0, j1, f0, f1, q0, q1;
+  fadd2(x0, x1, kShift, kShift, t0, t1);
+  fadd2(t0, t1, -kShift, -kShift, j0, j1);
+  ffma2(j0, j1, -1.f, -1.f, x0, x1, f0, f1);  // f = x - j
+  ffma2(a5, a5, f0, f1, a4, a4, q0, q1);
+  ffma2(q0, q1, f0, f1, a3, a3, q0, q1);
+  ffma2(q0, q1, f0, f1, a2, a2, q0, q1);
+  ffma2(q0, q1, f0, f1, a1, a1, q0, q1);
+  ffma2(q0, q1, f0, f1, a0, a0, q0, q1);
+  p0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
+  p1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
+}
+
 // HD: head size of Q and K; HDV: head size of V and the output (HDV <= HD).
 template <int HD, int HDV, bool F16>
 struct Cfg {
@@ -157,7 +178,6 @@ struct Unit {
 };
 
 constexpr int kUnitSlots = 4;    // decoded items the TMA warp may run ahead
-constexpr int kUnitReaders = 9;  // the MMA warp and the eight softmax warps read each item
 
 struct Barriers {
   uint64_t kv_full[8];
@@ -169,13 +189,16 @@ struct Barriers {
   uint64_t o_done[2];
   uint64_t drain;
   uint64_t stall;  // never arrived on (the test build waits on it)
+  // attn_fwd_sinks: a Q tile's scores are in registers; its last product with V is in O
+  uint64_t s_read[2];
+  uint64_t pv_done[2];
   uint64_t unit_full[kUnitSlots];   // an item (or the end mark) is in the slot
   uint64_t unit_empty[kUnitSlots];  // every reader has taken the slot's item
   Unit units[kUnitSlots];
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(Barriers) <= 512, "the barrier area of the shared-memory layout");
+static_assert(sizeof(Barriers) <= 1024, "the barrier area of the shared-memory layout");
 
 // Bounded wait on an mbarrier phase. Returns false (after recording a timeout, or when another
 // role of this block already gave up) instead of waiting forever.
@@ -358,6 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     FwdArgs a, int units_per_seq,
                     float scale_log2, int n_items, int* sched) {
   using C = Cfg<HD, HDV, F16>;
+  // attn_fwd_sinks at head size 64: tensor memory has room for P beside S, [384, 448) and [448, 512)
+  constexpr bool kOwnP = EXT == 3 && HDV == 64;
+  constexpr int kIssuers = kOwnP ? 2 : 1;  // warps that issue MMAs (they and the softmax warps read each item)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kBarOff);
@@ -369,20 +395,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar_addr(&bars->kv_full[s]), 1);
-      mbar_init(bar_addr(&bars->kv_empty[s]), 1);
+      mbar_init(bar_addr(&bars->kv_empty[s]), kIssuers);
     }
     mbar_init(bar_addr(&bars->q_full), 1);
-    mbar_init(bar_addr(&bars->q_empty), 1);
-    mbar_init(bar_addr(&bars->drain), 1);
+    mbar_init(bar_addr(&bars->q_empty), kIssuers);
+    mbar_init(bar_addr(&bars->drain), kIssuers);
     mbar_init(bar_addr(&bars->stall), 1);
     for (int q = 0; q < 2; ++q) {
       mbar_init(bar_addr(&bars->s_full[q]), 1);
       mbar_init(bar_addr(&bars->p_ready[q]), 4);  // one arrival per softmax warp
       mbar_init(bar_addr(&bars->o_done[q]), 1);
+      mbar_init(bar_addr(&bars->s_read[q]), 4);
+      mbar_init(bar_addr(&bars->pv_done[q]), 1);
     }
     for (int s = 0; s < kUnitSlots; ++s) {
       mbar_init(bar_addr(&bars->unit_full[s]), 1);
-      mbar_init(bar_addr(&bars->unit_empty[s]), kUnitReaders);
+      mbar_init(bar_addr(&bars->unit_empty[s]), 8 + kIssuers);
     }
     bars->abort = 0;
     fence_mbar_init();
@@ -493,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_bar(bar_addr(&bars->kv_full[i % C::kStages]), (i / C::kStages) & 1, abort, a.status, false);
         if (qn > 0) wait_bar(bar_addr(&bars->q_full), (qn - 1) & 1, abort, a.status, false);
       }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || (kOwnP && warp == kMmaWarp + 2)) {
       // =============================== MMA issue ==========================================
       if (lane == 0) {
         const uint32_t S0 = tmem, S1 = tmem + 128, O0 = tmem + 256, O1 = tmem + 256 + HDV;
@@ -525,6 +553,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t it = 0;        // K/V tiles consumed (the same sequence the TMA warp issues)
         int qn = 0;             // Q loads consumed
         uint32_t pc0 = 0, pc1 = 0;  // P hand-offs taken from each softmax warpgroup
+        if constexpr (kOwnP) {
+          // With P in columns of its own a Q tile's next scores are computed as soon as the current ones have
+          // been read, not after the product of P with V: a softmax warpgroup waited 1,500 of its 3,800
+          // cycles a tile for them (16 heads of 64, 2,047 rows, window 4,096: 79 -> 69 us). Each Q tile's
+          // products are issued by a warp of its own, since its two hand-offs come at times of their own.
+          // At head size 128 S, P and O fill tensor memory; there two issuing warps were slower than one
+          // (0.187 -> 0.224 ms for the packed case), as were tiles of 64 keys in two buffers.
+          const int q = warp == kMmaWarp ? 0 : 1;
+          const uint32_t Sq = q == 0 ? S0 : S1, Oq = q == 0 ? O0 : O1, Pq = tmem + 384 + q * 64;
+          const uint64_t dq = q == 0 ? dq0 : dq1;
+          uint32_t pc = 0;     // P hand-offs taken
+          uint32_t rc = 0;     // scores known to have been read
+          uint32_t sc = 0;     // scores issued
+          for (int k = 0; ok; ++k) {
+            const int slot = k % kUnitSlots;
+            if (!(ok = wait_bar(bar_addr(&bars->unit_full[slot]), (k / kUnitSlots) & 1, abort, a.status))) break;
+            const Unit* us = &bars->units[slot];
+            const int ub = us->b, n1 = us->n1, ns = us->ns;
+            // this Q tile's key tiles: those of the sinks and s .. n-1
+            const int s = q == 0 ? 0 : us->s1, n = q == 0 ? us->n0 : us->rows1 > 0 ? n1 : 0;
+            mbar_arrive(bar_addr(&bars->unit_empty[slot]));
+            if (ub < 0) break;
+            if (n1 <= 0) continue;
+            const int first = ns > 0 ? 0 : s;
+            auto act = [&](int j) { return j < n && (j >= s || j < ns); };
+            // scores of key tile j, and its K tile (the ring's tile it + 2 j) released
+            auto scores = [&](int j) -> bool {
+              const uint32_t ik = it + 2 * j;
+              if (!full(ik)) return false;
+              if (act(j)) {
+                if (sc != rc) {
+                  if (!wait_bar(bar_addr(&bars->s_read[q]), rc & 1, abort, a.status)) return false;
+                  ++rc;
+                }
+                tc_fence_after();
+                issue_qk(Sq, dq, ik);
+                mma_commit(bar_addr(&bars->s_full[q]));
+                ++sc;
+              }
+              if (j == n1 - 1) mma_commit(bar_addr(&bars->q_empty));
+              release(ik);
+              return true;
+            };
+            // O += P V for key tile j, and its V tile released
+            auto values = [&](int j) -> bool {
+              const uint32_t iv = it + 2 * j + 1;
+              if (!full(iv)) return false;
+              if (act(j)) {
+                if (!wait_bar(bar_addr(&bars->p_ready[q]), pc & 1, abort, a.status)) return false;
+                ++pc;
+                tc_fence_after();
+                issue_pv(Oq, Pq, iv, j > first);
+                mma_commit(bar_addr(&bars->pv_done[q]));
+                if (j == n - 1) mma_commit(bar_addr(&bars->o_done[q]));
+              }
+              release(iv);
+              return true;
+            };
+            ok = wait_bar(bar_addr(&bars->q_full), qn & 1, abort, a.status);
+            ++qn;
+            if (ok) ok = scores(0);
+            for (int j = 0; ok && j < n1; ++j) {
+              if (j + 1 < n1) ok = scores(j + 1);
+              if (ok) ok = values(j);
+            }
+            it += 2 * n1;
+          }
+        } else {
         for (int k = 0; ok; ++k) {
           const int slot = k % kUnitSlots;
           if (!(ok = wait_bar(bar_addr(&bars->unit_full[slot]), (k / kUnitSlots) & 1, abort, a.status))) break;
@@ -596,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           it += 2 * n1;
         }
+        }
         if (!ok) *abort = 1;
         // every MMA and commit issued above must have completed before TMEM is freed
         mma_commit(bar_addr(&bars->drain));
@@ -611,6 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t S = tmem + lane_off + q * 128;
     const uint32_t O = tmem + lane_off + 256 + q * HDV;
+    const uint32_t P = kOwnP ? tmem + lane_off + 384 + q * 64 : S;
+    uint32_t pvc = 0;  // kOwnP: tiles handed to the product with V
     uint32_t sfc = 0;  // S hand-offs taken, over all of the block's items
     uint32_t odc = 0;  // final-O hand-offs taken
     for (int k = 0;; ++k) {
@@ -682,6 +781,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32f(S + c * 32, s[c]);
           tmem_wait_ld();
+          if constexpr (kOwnP) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_addr(&bars->s_read[q]));
+          }
           if constexpr (EXT == 0) {
             if (kbase + kBN > lim) {
               const int hi = lim - kbase;  // this row's first masked column of the tile
@@ -752,7 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 x = __ffma2_rn(make_float2(s[c >> 5][c & 31], s[c >> 5][(c + 1) & 31]), sc2, nm2);
             float p0, p1;
             if (kEmuEvery > 0 && ((c >> 1) % (kEmuEvery > 0 ? kEmuEvery : 1)) == kEmuEvery - 1) {
-              exp2_poly2(x.x, x.y, p0, p1);
+              if constexpr (EXT == 3) exp2_poly5(x.x, x.y, p0, p1);
+              else exp2_poly2(x.x, x.y, p0, p1);
             } else {
               p0 = ex2(x.x);
               p1 = ex2(x.y);
@@ -761,7 +866,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[c >> 6][(c >> 1) & 31] = pack16x2<F16>(p0, p1);
             // the first 64 keys' P go to TMEM (over S columns already read) as soon as they
             // are packed, so that half of P need not stay in registers
-            if (c == 62) tmem_st32(S, pk[0]);
+            if (c == 62) {
+              if constexpr (kOwnP) {
+                // the product of the last P with V has read it (and is in O, which the rescaling below needs)
+                if (pvc > 0)
+                  ok = __all_sync(0xffffffffu, wait_bar(bar_addr(&bars->pv_done[q]), (pvc - 1) & 1, abort, a.status));
+                tc_fence_after();
+              }
+              tmem_st32(P, pk[0]);
+            }
           }
           l += ((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y)) + ((rs[2].x + rs[2].y) + (rs[3].x + rs[3].y));
           // rescale O (complete up to tile j-1: the S_j commit covers every earlier MMA)
@@ -777,11 +890,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st32(O + c * 32, o);
             }
           }
-          tmem_st32(S + 32, pk[1]);
+          tmem_st32(P + 32, pk[1]);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_addr(&bars->p_ready[q]));
+          if constexpr (kOwnP) {
+            ++pvc;
+            if (!ok) break;
+          }
         }
       }
       // ---- epilogue: O / l -> bf16, statistics ------------------------------------------------
