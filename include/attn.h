@@ -13,8 +13,8 @@
  *                    caller-owned buffer that attn_sparse_csr_tc_planned then reads.
  *   attn_fwd_sinks   attn_fwd through a sliding window of the newest keys and the first few keys.
  *   attn_decode_paged  the same for one new token per sequence, over a paged key/value cache.
- *   attn_cache_append, attn_cache_fork, attn_cache_reserve, attn_cache_copy, attn_cache_compact
- *                    that cache: new tokens written into its pages, and the bookkeeping of the pages.
+ *   attn_cache_append, attn_cache_fork, attn_cache_reserve, attn_cache_evict, attn_cache_compact,
+ *   attn_cache_copy  that cache: new tokens written into its pages, and the bookkeeping of the pages.
  *
  * Conventions shared by every call
  *   - All tensor pointers are DEVICE pointers owned by the caller. The library allocates no
@@ -375,7 +375,7 @@ ATTN_API int attn_fwd_sinks(const void* q, const void* k, const void* v,
  * attn_cache_append) and sees the keys that attn_fwd_sinks's rule gives that position: with
  * ATTN_WINDOW_ALL all seq_lens[b] of them. GQA, scale and statistics are attn_fwd's. A row of length 0
  * gives out 0, max -inf, sum 0. Only visible positions are read: table entries between the sinks and
- * the window may be -1 (their pages freed), and what lies in a page behind the last token, or in
+ * the window may be -1 (attn_cache_evict), and what lies in a page behind the last token, or in
  * positions that are not seen, may hold anything, NaN included.
  * ATTN_BF16 and ATTN_F16 with D = 64 or 128, 16-byte aligned q, caches and page_stride run on the
  * tensor cores (products exact, sums in float32, probabilities kept to 16 bits or more); other head
@@ -449,6 +449,19 @@ ATTN_API int attn_cache_fork(const int32_t* page_table, const int32_t* src_rows,
 ATTN_API int attn_cache_reserve(int32_t* page_table, int32_t* ref_count, const int32_t* seq_lens,
                                 const int32_t* new_tokens, int B, int max_pages, int num_pages,
                                 int page_size, int32_t* copies, void* stream);
+
+/*
+ * attn_cache_evict -- let go of pages that a window has left behind, in place.
+ *
+ * Frees each table entry [b, i] all of whose positions i * page_size .. (i + 1) * page_size - 1 lie
+ * behind the first sink_tokens ones and before the window of position seq_lens[b] - 1: no query at that
+ * position or a later one sees them (attn_decode_paged with the same window_tokens and sink_tokens).
+ * The entry becomes -1 and its page loses a holder. With ATTN_WINDOW_ALL nothing is freed.
+ * Data errors: a row whose length is outside its range, and entries >= num_pages, are left as they are.
+ */
+ATTN_API int attn_cache_evict(int32_t* page_table, int32_t* ref_count, const int32_t* seq_lens, int B,
+                              int max_pages, int num_pages, int page_size, int64_t window_tokens,
+                              int64_t sink_tokens, void* stream);
 
 /*
  * attn_cache_compact -- plan the moves that bring all live pages to the front of the pool.

@@ -2,8 +2,8 @@
 
 The operations (attn_fwd, attn_fwd_masked, attn_fwd_accumulate, attn_sparse_csr,
 attn_sparse_csr_tc, attn_csr_plan_size, attn_csr_plan, attn_sparse_csr_tc_planned, attn_merge,
-attn_fwd_sinks, attn_decode_paged, attn_cache_append, attn_cache_fork, attn_cache_reserve,
-attn_cache_compact, attn_cache_copy, attn_get_last_error) are the C-ABI calls declared in
+attn_fwd_sinks, attn_decode_workspace_size, attn_decode_paged, attn_cache_append, attn_cache_fork,
+attn_cache_reserve, attn_cache_evict, attn_cache_compact, attn_cache_copy, attn_get_last_error) are the C-ABI calls declared in
 ``include/attn.h``; the functions here carry the same names and only marshal arguments (tensor
 data pointers, sizes, the current CUDA stream) into them. Every step of the computation runs in the library's CUDA kernels.
 There is no CPU path: if ``libattn.so`` is missing the first call raises.
@@ -25,7 +25,7 @@ __all__ = [
     "load_library", "attn_fwd_masked", "attn_sparse_csr_tc", "attn_csr_plan_size", "attn_csr_plan",
     "attn_sparse_csr_tc_planned", "attn_sparse_csr_tc_noalloc", "attn_fwd_sinks",
     "attn_decode_workspace_size", "attn_decode_paged", "attn_cache_append", "attn_cache_fork",
-    "attn_cache_reserve", "attn_cache_compact", "attn_cache_copy", "ATTN_WINDOW_ALL",
+    "attn_cache_reserve", "attn_cache_evict", "attn_cache_compact", "attn_cache_copy", "ATTN_WINDOW_ALL",
 ]
 
 (ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_DATA, ATTN_ERR_TIMEOUT,
@@ -96,6 +96,8 @@ def load_library():
         lib.attn_cache_fork.restype = I
         lib.attn_cache_reserve.argtypes = [P, P, P, P, I, I, I, I, P, P]
         lib.attn_cache_reserve.restype = I
+        lib.attn_cache_evict.argtypes = [P, P, P, I, I, I, I, I64, I64, P]
+        lib.attn_cache_evict.restype = I
         lib.attn_cache_compact.argtypes = [P, P, I, I, I, P, P, P, P, P, P]
         lib.attn_cache_compact.restype = I
         lib.attn_cache_copy.argtypes = [P, I, I, I64, I64, I, P, P, P]
@@ -513,6 +515,20 @@ def attn_cache_reserve(page_table, ref_count, seq_lens, new_tokens, copies, *, B
         _arg(copies, "copies", 2 * B, i32, dev), _on(stream, dev))
     if rc:
         _check(rc, "attn_cache_reserve")
+
+
+def attn_cache_evict(page_table, ref_count, seq_lens, *, B: int, max_pages: int, num_pages: int, page_size: int,
+                     window_tokens: int, sink_tokens: int = 0, stream=None) -> None:
+    """Let go of pages that a window has left behind, in place (see ``attn_cache_evict`` in
+    include/attn.h)."""
+    lib, dev = _lib or load_library(), _here()
+    i32 = _DEV["i32"]
+    rc = lib.attn_cache_evict(
+        _arg(page_table, "page_table", B * max_pages, i32, dev), _arg(ref_count, "ref_count", num_pages, i32, dev),
+        _arg(seq_lens, "seq_lens", B, i32, dev), B, max_pages, num_pages, page_size, window_tokens, sink_tokens,
+        _on(stream, dev))
+    if rc:
+        _check(rc, "attn_cache_evict")
 
 
 def attn_cache_compact(page_table, ref_count, page_table_out, ref_count_out, page_map, copies, live_pages, *,

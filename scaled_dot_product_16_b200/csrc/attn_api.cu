@@ -583,6 +583,31 @@ int attn_cache_reserve(int32_t* page_table, int32_t* ref_count, const int32_t* s
   return from_cuda(sdpa::launch_cache_reserve(a, static_cast<cudaStream_t>(stream)));
 }
 
+int attn_cache_evict(int32_t* page_table, int32_t* ref_count, const int32_t* seq_lens, int B, int max_pages,
+                     int num_pages, int page_size, int64_t window_tokens, int64_t sink_tokens, void* stream) {
+  int rc = table_args(B, max_pages, num_pages);
+  if (rc != ATTN_OK) return rc;
+  if (page_size < 1 || window_tokens < 1 || sink_tokens < 0) return ATTN_ERR_INVALID;
+  if ((int64_t)max_pages * page_size > (int64_t(1) << 30)) return ATTN_ERR_UNSUPPORTED;
+  if ((int64_t)B * max_pages == 0) return ATTN_OK;
+  if (seq_lens == nullptr || page_table == nullptr) return ATTN_ERR_INVALID;
+  if (num_pages > 0 && ref_count == nullptr) return ATTN_ERR_INVALID;
+  sdpa::EvictArgs a{};
+  a.table = page_table;
+  a.ref = ref_count;
+  a.lens = seq_lens;
+  a.B = B;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.window = clamp30(window_tokens);
+  a.sinks = clamp30(sink_tokens);
+  int sms = 0;
+  rc = device_state(&a.status, &sms);
+  if (rc != ATTN_OK) return rc;
+  return from_cuda(sdpa::launch_cache_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
 int attn_cache_compact(const int32_t* page_table, const int32_t* ref_count, int rows, int max_pages,
                        int num_pages, int32_t* page_table_out, int32_t* ref_count_out, int32_t* page_map,
                        int32_t* copies, int32_t* live_pages, void* stream) {

@@ -1,5 +1,5 @@
 // cache_pages.cu -- the pages of a key/value cache: writing new tokens into them, and the bookkeeping
-// that forks, frees, reserves and compacts them.
+// that forks, frees, reserves, evicts and compacts them.
 //
 // The state is a page table [rows, max_pages] (-1: no page) and a reference count per page (0: free).
 // Everything is decided on the device from these arrays, so a serving step never waits for the host
@@ -103,7 +103,7 @@ cudaError_t launch_append(AppendArgs a, int es, cudaStream_t st) {
 // ---- attn_cache_copy -----------------------------------------------------------------------------
 // Each block takes (pair, chunk) items in turn; bound by HBM (a page's bytes read and written once).
 constexpr int kCopyThreads = 256;
-constexpr int kCopyVecs = 4;  // vectors a thread holds of each of k and v
+constexpr int kCopyVecs = 8;  // vectors a thread holds of each of k and v
 
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(PageCopyArgs a, int64_t page_vecs, int64_t stride_vecs,
@@ -444,6 +444,29 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
   }
 }
 
+// ---- attn_cache_evict ----------------------------------------------------------------------------
+// One thread per table entry; only those between the sinks and the window look at the table.
+__global__ void __launch_bounds__(256) evict_kernel(EvictArgs a, int64_t n) {
+  for (int64_t x = blockIdx.x * 256LL + threadIdx.x; x < n; x += gridDim.x * 256LL) {
+    const int b = (int)(x / a.max_pages), i = (int)(x - (int64_t)b * a.max_pages);
+    const int len = __ldg(a.lens + b);
+    if (len < 0 || len > a.max_pages * a.page_size) {
+      if (i == 0) report(a.status, ATTN_ERR_DATA);
+      continue;
+    }
+    const int p0 = i * a.page_size;
+    if (len <= a.window || p0 < a.sinks || p0 + a.page_size > len - a.window) continue;
+    const int page = a.table[x];
+    if (page < 0) continue;
+    if (page >= a.num_pages) {
+      report(a.status, ATTN_ERR_DATA);
+      continue;
+    }
+    a.table[x] = -1;
+    atomicSub(a.ref + page, 1);
+  }
+}
+
 // ---- attn_cache_compact --------------------------------------------------------------------------
 // One block scans the counts: with n live pages, the k-th live page at or above n moves to the k-th
 // free page below n. It renames the pages of a small table too; a second kernel, of more blocks, those of
@@ -570,14 +593,22 @@ cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t st) {
   int cols = kForkEntries / rows;
   cols = cols < 1 ? 1 : (cols > 32 ? 32 : cols);
   const int smem = (int)sizeof(int32_t) * (a.rows_in + a.rows_in * cols);
-  cudaError_t e = cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {  // a column of more than 6,144 rows
+    const cudaError_t e = cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   fork_kernel<<<(a.max_pages + cols - 1) / cols, kForkThreads, smem, st>>>(a, cols);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_reserve(const ReserveArgs& a, cudaStream_t st) {
   reserve_kernel<<<1, kResThreads, sizeof(int32_t) * a.B, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st) {
+  const int64_t n = (int64_t)a.B * a.max_pages, blocks = (n + 255) / 256;
+  evict_kernel<<<(unsigned)(blocks < 2048 ? blocks : 2048), 256, 0, st>>>(a, n);
   return cudaGetLastError();
 }
 

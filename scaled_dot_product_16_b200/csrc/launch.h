@@ -149,6 +149,15 @@ struct ReserveArgs {
   int* status;
 };
 
+struct EvictArgs {
+  int32_t* table;
+  int32_t* ref;
+  const int32_t* lens;
+  int B, max_pages, num_pages, page_size;
+  int window, sinks;  // clamped to 2^30
+  int* status;
+};
+
 struct CompactArgs {
   const int32_t* table;
   const int32_t* ref;
@@ -181,6 +190,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t st);
 cudaError_t launch_cache_reserve(const ReserveArgs& a, cudaStream_t st);
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st);
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st);
 cudaError_t launch_cache_copy(const PageCopyArgs& a, cudaStream_t st);
 cudaError_t launch_merge(const MergeArgs& a, cudaStream_t st);

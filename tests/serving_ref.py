@@ -177,3 +177,15 @@ def live_table(rng, lens, page_size, max_pages, num_pages, share=0):
                 ref[p] += 1
         table.append(row)
     return table, ref
+
+
+def evict(table, ref, lens, page_size, window, sinks):
+    """Table and counts afterwards."""
+    table, ref = [list(r) for r in table], list(ref)
+    for row, n in zip(table, lens):
+        for i, p in enumerate(row):
+            gone = all(sinks <= j < n - window for j in range(i * page_size, (i + 1) * page_size))
+            if 0 <= p < len(ref) and gone:
+                row[i] = -1
+                ref[p] -= 1
+    return table, ref

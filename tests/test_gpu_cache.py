@@ -288,3 +288,186 @@ def test_copy_bad_pairs_are_skipped():
     status(sdpa.ATTN_ERR_DATA)
     base[3] = base[0]
     assert torch.equal(k.cpu(), base) and torch.equal(v.cpu(), base)
+
+
+# ---- evict -----------------------------------------------------------------------------------------
+@pytest.mark.parametrize("page", [1, 4, 16])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (7, 3), (16, 16), (40, 1), (3, 1000), (sdpa.ATTN_WINDOW_ALL, 2)])
+def test_evict(page, window, sinks):
+    rng = np.random.default_rng(page)
+    lens = [0, 1, 15, 16, 17, 64, 100, 100, 100]
+    mp = 100 // page + 2
+    num = sum(-(-n // page) for n in lens) + 3
+    table, ref = R.live_table(rng, lens, page, mp, num)
+    table, ref, lens = R.fork(table, [0, 1, 2, 3, 4, 5, 6, 6, 8], ref, lens, num)  # row 7 shares row 6's pages
+    t, r = dev(table), dev(ref)
+    sdpa.attn_cache_evict(t, r, dev(lens), B=9, max_pages=mp, num_pages=num, page_size=page, window_tokens=window,
+                          sink_tokens=sinks)
+    status()
+    want = R.evict(table, ref, lens, page, window, sinks)
+    assert t.tolist() == want[0] and r.tolist() == want[1]
+
+
+def test_evict_bad_data():
+    table, ref = [[0, 1, 9], [2, 3, 4]], [1] * 6
+    t, r = dev(table), dev(ref)
+    sdpa.attn_cache_evict(t, r, dev([12, 13]), B=2, max_pages=3, num_pages=6, page_size=4, window_tokens=1)
+    status(sdpa.ATTN_ERR_DATA)  # row 1 is longer than its table
+    assert t.tolist() == [[-1, -1, 9], [2, 3, 4]] and r.tolist() == [0, 0, 1, 1, 1, 1]
+    t, r = dev([[0, 7, 2]]), dev(ref)
+    sdpa.attn_cache_evict(t, r, dev([12]), B=1, max_pages=3, num_pages=6, page_size=4, window_tokens=1)
+    status(sdpa.ATTN_ERR_DATA)
+    assert t.tolist() == [[-1, 7, 2]] and r.tolist() == [0, 1, 1, 1, 1, 1]
+
+
+# ---- all of them together ---------------------------------------------------------------------------
+class Model:
+    """The keys and values of each row as plain lists, beside a PagedCache of two layers."""
+
+    def __init__(self, cache, dtype, seed):
+        self.cache, self.dtype, self.seed = cache, dtype, seed
+        self.kv = [[([], []) for _ in range(cache.rows)] for _ in range(cache.layers)]
+
+    def draw(self, shape):
+        self.seed += 1
+        return W.randn(shape, self.seed).to(self.dtype)
+
+    def step(self, new):
+        """Adds new[b] tokens to each row in both layers; returns the packed (k, v) of each."""
+        c = self.cache
+        out = []
+        for layer in range(c.layers):
+            k, v = self.draw((sum(new), c.Nkv, c.D)), self.draw((sum(new), c.Nkv, c.D))
+            t = 0
+            for b, n in enumerate(new):
+                for i in range(t, t + n):
+                    self.kv[layer][b][0].append(k[i])
+                    self.kv[layer][b][1].append(v[i])
+                t += n
+            out.append((k, v))
+        return out
+
+    def fork(self, src):
+        for layer in range(self.cache.layers):
+            old = self.kv[layer]
+            self.kv[layer] = [(list(old[s][0]), list(old[s][1])) if s >= 0 else ([], []) for s in src]
+
+    def attend(self, layer, q):
+        c = self.cache
+        out, A = torch.zeros(q.shape, dtype=torch.float64), torch.zeros(q.shape, dtype=torch.float64)
+        for b in range(c.rows):
+            ks, vs = self.kv[layer][b]
+            if not ks:
+                continue
+            k, v = torch.stack(ks), torch.stack(vs)
+            seen = R.window_seen(1, len(ks), c.window_tokens, c.sink_tokens)
+            for h in range(c.Nq):
+                g = h // (c.Nq // c.Nkv)
+                o, _, _, a, _ = R.attend(q[b, h][None], k[:, g], v[:, g], seen, c.scale)
+                out[b, h], A[b, h] = o[0], a[0]
+        return out.numpy(), A.numpy()
+
+
+@pytest.mark.parametrize("dtype,layout,D,window,sinks", [
+    (BF, W.TND, 128, sdpa.ATTN_WINDOW_ALL, 0), (F16, W.BHSD, 64, 40, 5), (F32, W.TND, 40, 24, 0),
+    (BF, W.BHSD, 64, 30, 40)], ids=["bf16", "f16-window", "f32-window", "bf16-sinks"])
+def test_serving_from_prompts_to_beams(dtype, layout, D, window, sinks):
+    """Prompts through the windowed forward into the cache, tokens one by one, forks as beam search makes
+    them, eviction, compaction and rows that end, in two layers that share the table; after every step
+    attention over the pages is that over the rows' own lists of keys and values."""
+    from scaled_dot_product_16_b200.cache import PagedCache
+    rng = np.random.default_rng(D)
+    rows, Nq, Nkv = 6, 8, 2
+    cache = PagedCache(layers=2, rows=rows, max_pages=24, num_pages=90, page_size=8, Nq=Nq, Nkv=Nkv, D=D,
+                       dtype=W.dtype_code(dtype), layout=layout, window_tokens=window, sink_tokens=sinks)
+    cache.pool.fill_(float("nan"))  # nothing that was not written is seen
+    model = Model(cache, dtype, 100 * D)
+
+    def attend():
+        for layer in range(2):
+            q = model.draw((rows, Nq, D))
+            out = G.Guarded(tuple(q.shape), dtype)
+            cache.attend(layer, q.cuda(), out.t)
+            cache.check()
+            out.check()
+            ref, A = model.attend(layer, q)
+            G.check_out(G.f64(out.t.cpu()), ref, W.dtype_code(dtype), abs_ref=A)
+
+    new = [50, 1, 0, 83, 16, 7]
+    cache.reserve(dev(new))
+    cu = dev(np.cumsum(new).tolist())
+    for layer, (k, v) in enumerate(model.step(new)):
+        q = model.draw((sum(new), Nq, D))
+        out = G.Guarded(tuple(q.shape), dtype)
+        cache.prefill(layer, q.cuda(), k.cuda(), v.cuda(), cu, out.t)
+        cache.check()
+        out.check()
+        inp = W.AttnInputs(q, k, v, W.TND, 0, W.dtype_code(dtype), rows, sum(new), sum(new), Nq, Nkv, D, cache.scale,
+                           np.cumsum(new).astype(np.int32), np.cumsum(new).astype(np.int32))
+        ref, _, _, A = R.window_fwd(inp, window, sinks)
+        G.check_out(G.f64(out.t.cpu()), ref, inp.dtype, abs_ref=A)
+    attend()
+    for step in range(8):
+        cache.reserve()
+        for layer, (k, v) in enumerate(model.step([1] * rows)):
+            cache.append(layer, k.cuda(), v.cuda())
+        attend()
+        if step == 5:
+            src = [0, 1, 2, -1, 4, 4]   # a row ends, one is forked
+        else:
+            src = [int(x) for x in rng.integers(0, rows, rows)]
+        cache.fork(dev(src))
+        model.fork(src)
+        if step % 3 == 1 and window < 100:
+            cache.evict()
+        if step % 3 == 2:
+            cache.compact()
+            cache.check()
+            n = int(cache.live_pages)
+            assert (cache.ref_count[:n] > 0).all() and not cache.ref_count[n:].any()
+        held = cache.page_table[cache.page_table >= 0].long()
+        assert torch.equal(torch.bincount(held, minlength=90).int(), cache.ref_count)
+        attend()
+    cache.fork(dev([-1] * rows))
+    cache.check()
+    assert not cache.ref_count.any() and not cache.seq_lens.any() and bool((cache.page_table == -1).all())
+    cache.reserve(dev([24 * 8] * rows))   # more pages than there are
+    with pytest.raises(sdpa.AttnError, match="pages"):
+        cache.check()
+
+
+def test_a_step_captured_into_a_graph():
+    """reserve, append and attend recorded once and replayed token by token."""
+    from scaled_dot_product_16_b200.cache import PagedCache
+    rows, Nq, Nkv, D = 4, 4, 2, 64
+    cache = PagedCache(layers=1, rows=rows, max_pages=6, num_pages=30, page_size=4, Nq=Nq, Nkv=Nkv, D=D, dtype=W.BF16)
+    model = Model(cache, BF, 5)
+    q, k, v = (torch.zeros((rows, n, D), dtype=BF, device="cuda") for n in (Nq, Nkv, Nkv))
+    out = torch.empty_like(q)
+
+    def step():
+        cache.reserve()
+        cache.append(0, k, v)
+        cache.attend(0, q, out)
+
+    step()                       # once outside the capture; then from the start again
+    cache.fork(dev([-1] * rows))
+    cache.check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    cache.fork(dev([-1] * rows))
+    for i in range(20):
+        (kn, vn), = model.step([1] * rows)
+        qn = model.draw((rows, Nq, D))
+        q.copy_(qn), k.copy_(kn), v.copy_(vn)
+        if i == 7:
+            cache.fork(dev([0, 0, 2, 1]))
+            model.fork([0, 0, 2, 1])
+            for b in range(rows):  # the step's own token is the one drawn for the row
+                model.kv[0][b] = (model.kv[0][b][0][:-1] + [kn[b]], model.kv[0][b][1][:-1] + [vn[b]])
+        g.replay()
+        cache.check()
+        ref, A = model.attend(0, qn)
+        G.check_out(G.f64(out.cpu()), ref, W.BF16, abs_ref=A)
+    assert cache.seq_lens.tolist() == [20] * rows

@@ -129,6 +129,16 @@ def test_page_calls(lib):
         assert c(**bad) == INVALID, bad
     assert c(rows=8193) == UNSUP
 
+    ev = dict(table=16, ref=16, lens=16, B=2, max_pages=4, num_pages=9, page_size=16, window=8, sinks=0, stream=None)
+
+    def e(**kw):
+        return _call(lib.attn_cache_evict, ev, kw)
+
+    for bad in (dict(B=-1), dict(page_size=0), dict(window=0), dict(sinks=-1), dict(table=None), dict(ref=None),
+                dict(lens=None), dict(max_pages=-1)):
+        assert e(**bad) == INVALID, bad
+    assert e(B=8193) == UNSUP and e(page_size=1 << 29) == UNSUP and e(B=0) == OK
+
     cp = dict(copies=16, n=2, num_pages=9, page_elems=64, stride=0, dtype=0, k=16, v=16, stream=None)
 
     def p(**kw):
