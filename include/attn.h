@@ -339,8 +339,9 @@ ATTN_API int attn_merge(const void* prev_out, const float* prev_max, const float
  * sink_tokens >= 0. Key tiles between the sinks and a block's windows are neither read nor
  * multiplied, so the cost grows with window_tokens + sink_tokens and not with Skv.
  * Other arguments, layouts, statistics, limits and errors are those of attn_fwd.
- * NaN or infinite values at keys that a row does not see do not reach the row's scores; in the
- * values v they may (0 * NaN) reach rows whose key tiles (128 keys; 32 for ATTN_F32) hold them.
+ * NaN or infinite values in keys that a row does not see do not reach the row. In values of its own
+ * sequence that it does not see they may (0 * NaN), where a key tile (128 keys; 32 for ATTN_F32) holds
+ * them beside keys that rows of its block see; those of other sequences never do.
  */
 ATTN_API int attn_fwd_sinks(const void* q, const void* k, const void* v,
                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,

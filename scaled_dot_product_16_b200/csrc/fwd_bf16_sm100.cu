@@ -192,6 +192,7 @@ struct Barriers {
   // attn_fwd_sinks: a Q tile's scores are in registers; its last product with V is in O
   uint64_t s_read[2];
   uint64_t pv_done[2];
+  uint64_t scrub[8];  // a V tile that also holds rows of the next sequence is in this ring stage
   uint64_t unit_full[kUnitSlots];   // an item (or the end mark) is in the slot
   uint64_t unit_empty[kUnitSlots];  // every reader has taken the slot's item
   Unit units[kUnitSlots];
@@ -364,6 +365,15 @@ __device__ __forceinline__ bool decode_unit(const FwdArgs& a, int units_per_seq,
   return true;
 }
 
+// Rows of an item's last key tile that belong to its sequence, where the others are another sequence's
+// (packed batches with a window; kBN: none are).
+template <int EXT>
+__device__ __forceinline__ int tile_rows(const FwdArgs& a, const Unit& U) {
+  if (EXT != 3 || a.layout == ATTN_BHSD || U.b < 0) return kBN;
+  const int rows = U.sk - key_tile<EXT>(U, U.n1 - 1) * kBN;
+  return rows < kBN ? rows : kBN;
+}
+
 // EXT: the masked-call features. 0: plain calls, whose softmax loop carries none of their code;
 // 1: the band's lower edge; 2: the band and an explicit mask (its bytes take registers that the
 // band alone does not need); 3: a window that ends at each row's position and the first keys
@@ -383,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<HD, HDV, F16>;
   // attn_fwd_sinks at head size 64: tensor memory has room for P beside S, [384, 448) and [448, 512)
   constexpr bool kOwnP = EXT == 3 && HDV == 64;
+  constexpr int kScrubbers = EXT == 3 ? 1 : 0;
   constexpr int kIssuers = kOwnP ? 2 : 1;  // warps that issue MMAs (they and the softmax warps read each item)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -401,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar_addr(&bars->q_empty), kIssuers);
     mbar_init(bar_addr(&bars->drain), kIssuers);
     mbar_init(bar_addr(&bars->stall), 1);
+    for (int s = 0; s < C::kStages; ++s) mbar_init(bar_addr(&bars->scrub[s]), 1);
     for (int q = 0; q < 2; ++q) {
       mbar_init(bar_addr(&bars->s_full[q]), 1);
       mbar_init(bar_addr(&bars->p_ready[q]), 4);  // one arrival per softmax warp
@@ -410,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kUnitSlots; ++s) {
       mbar_init(bar_addr(&bars->unit_full[s]), 1);
-      mbar_init(bar_addr(&bars->unit_empty[s]), 8 + kIssuers);
+      mbar_init(bar_addr(&bars->unit_empty[s]), 8 + kIssuers + kScrubbers);
     }
     bars->abort = 0;
     fence_mbar_init();
@@ -482,7 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto load_kv = [&](int i) {
               const uint32_t s = it % C::kStages, r = it / C::kStages;
               if (r > 0 && !wait_bar(bar_addr(&bars->kv_empty[s]), (r - 1) & 1, abort, a.status)) return false;
-              const uint32_t fb = bar_addr(&bars->kv_full[s]);
+              const bool scrub = EXT == 3 && i == nl - 1 && tile_rows<EXT>(a, U) < kBN;
+              const uint32_t fb = scrub ? bar_addr(&bars->scrub[s]) : bar_addr(&bars->kv_full[s]);
               mbar_arrive_expect_tx(fb, (i & 1) ? C::kTileBytesV : C::kTileBytes);
               load_tile((i & 1) ? &tm_v : &tm_k, sKV + s * C::kTileBytes, fb,
                         k0 + key_tile<EXT>(U, i >> 1) * kBN, khead,
@@ -520,6 +533,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = it > (uint32_t)C::kStages ? it - C::kStages : 0u; i < it; ++i)
           wait_bar(bar_addr(&bars->kv_full[i % C::kStages]), (i / C::kStages) & 1, abort, a.status, false);
         if (qn > 0) wait_bar(bar_addr(&bars->q_full), (qn - 1) & 1, abort, a.status, false);
+      }
+    } else if (EXT == 3 && warp == kMmaWarp + 3) {
+      // =============================== value rows of the next sequence ======================
+      // In a packed batch the last key tile of a sequence also holds tokens of the next one. Their weights
+      // are 0, but 0 times a NaN or an infinity there would reach this sequence: their value rows become
+      // zeros before the product with V reads them.
+      uint32_t it = 0, scrubs = 0;  // tiles of the items so far; a parity bit per ring stage
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const int slot = k % kUnitSlots;
+        if (!(ok = __all_sync(0xffffffffu, wait_bar(bar_addr(&bars->unit_full[slot]), (k / kUnitSlots) & 1, abort, a.status)))) break;
+        const Unit* us = &bars->units[slot];
+        const int ub = us->b, n1 = us->n1, first = n1 > 0 ? tile_rows<EXT>(a, *us) : kBN;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_addr(&bars->unit_empty[slot]));
+        if (ub < 0) break;
+        if (first < kBN) {
+          // the load of this tile completes on the stage's scrub barrier, and this warp fills the stage
+          const uint32_t st = (it + 2 * n1 - 1) % C::kStages;
+          ok = __all_sync(0xffffffffu, wait_bar(bar_addr(&bars->scrub[st]), (scrubs >> st) & 1, abort, a.status));
+          if (!ok) break;
+          scrubs ^= 1u << st;
+          const uint32_t tile = sKV + st * C::kTileBytes;  // rows of 128 bytes, a box of kBN rows per 64 columns
+          for (int x = lane; x < (kBN - first) * 8; x += 32)
+            for (int box = 0; box < C::kBoxesV; ++box)
+              st_shared_v4(tile + box * (kBN * 128) + (first + (x >> 3)) * 128 + (x & 7) * 16, 0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_addr(&bars->kv_full[st]));
+        }
+        it += 2 * n1;
       }
     } else if (warp == kMmaWarp || (kOwnP && warp == kMmaWarp + 2)) {
       // =============================== MMA issue ==========================================

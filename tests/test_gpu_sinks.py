@@ -107,6 +107,30 @@ def test_keys_left_out_may_hold_anything(dtype):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dtype", [BF, F16, F32], ids=IDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads", [(4, 2), (3, 3)])
+def test_a_sequence_of_nan_stays_by_itself(dtype, D, heads):
+    """NaN and infinities in one sequence of a packed batch leave the others as they were, bit for bit, though
+    their last key tiles hold its tokens."""
+    inp = W.varlen_tnd([300, 5, 129, 1, 700, 128], *heads, D, causal=False, dtype=dtype, seed=12, cfg=82)
+    cu = [0] + list(inp.cu_q)
+    for window, sinks in ((100, 4), (sdpa.ATTN_WINDOW_ALL, 0)):
+        want = _run(inp, window, sinks)
+        for bad in (1, 3, 5):
+            k, v = inp.k.clone(), inp.v.clone()
+            rows = slice(cu[bad], cu[bad + 1])
+            k[rows], v[rows] = float("nan"), float("inf") if bad == 3 else float("nan")
+            other = W.AttnInputs(inp.q, k, v, inp.layout, 0, inp.dtype, inp.B, inp.Sq, inp.Skv, inp.Nq, inp.Nkv, D,
+                                 inp.scale, inp.cu_q, inp.cu_kv)
+            got = _run(other, window, sinks)
+            keep = torch.ones(inp.Sq, dtype=torch.bool)
+            keep[rows] = False
+            for x, y in zip(want, got):
+                assert torch.equal(x[keep], y[keep]), (window, bad)
+            assert not torch.isfinite(got[0][~keep]).any()
+
+
 def test_large_scores_and_one_hot_rows():
     inp = W.dense_bhsd(1, 2, 300, 64, causal=False, dtype=BF, seed=9, cfg=79)
     inp.q = inp.q * 64
