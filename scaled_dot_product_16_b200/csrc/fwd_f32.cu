@@ -14,7 +14,7 @@
 //
 // The tiles come by asynchronous copies (16 bytes at a time where rows allow it), the next one while
 // the current one is multiplied: with plain loads a block of few key tiles spent most of its time
-// waiting for them (2 x 4 x 333 x 80, window 128: 121 us, now 20 us). Rows are padded to whole 16-byte chunks, so that
+// waiting for them (2 x 4 x 333 x 80, window 128: 121 us, now 28). Rows are padded to whole 16-byte chunks, so that
 // queries and keys are read four columns at a time, and the weights four rows at a time: the loop is
 // bound by shared-memory reads otherwise. The order of every sum is that of one column, and one key,
 // after the other.
@@ -28,7 +28,9 @@ namespace {
 
 constexpr int kBM = 32;       // query rows per block
 constexpr int kBN = 32;       // keys per tile
-constexpr int kWarps = 8;     // of 4 rows each: 4 warps of 8 rows read K less often but hide less (1.2-1.5 times the time)
+// Warps of a block, 4 rows each. 4 warps of 8 rows read K less often but hide less (1.2 to 1.5 times the
+// time), 16 of 2 rows are bound by the reads of K (1.3 to 1.6 times).
+constexpr int kWarps = 8;
 constexpr int kRowsPerWarp = kBM / kWarps;
 
 // 4 or 16 bytes to shared memory, or zeros where !ok (src is then not read)
@@ -180,10 +182,10 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
   if (j_first < kv_end) fetch(j_first, 0);
   asm volatile("cp.async.commit_group;" ::: "memory");
   for (int j0 = j_first; j0 < kv_end; j0 = after(j0), buf ^= 1) {
-    if (after(j0) < kv_end) fetch(after(j0), buf ^ 1);  // its last reader passed the barrier below
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // this tile is there (and Q, on the first pass), and the last one is consumed
+    if (after(j0) < kv_end) fetch(after(j0), buf ^ 1);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    __syncthreads();  // this tile is there (and Q, on the first pass)
 
     // scores: lane = key j0 + lane, one value per row of this warp
     float s[kRowsPerWarp];
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
     for (int r = 0; r < kRowsPerWarp; ++r) s[r] = 0.f;
     const float* kr = sK + buf * kBN * ldk + lane * ldk;
     const float* qr = sQ + warp * kRowsPerWarp * D4;
-#pragma unroll 4
+#pragma unroll 8
     for (int d = 0; d < D4; d += 4) {
       const float4 kv = *reinterpret_cast<const float4*>(kr + d);
 #pragma unroll
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
     __syncwarp();
     // P.V: lane owns head-dim columns lane, lane+32, ...
     const float* vt = sV + buf * kBN * Dv4;
-#pragma unroll 4
+#pragma unroll 8
     for (int jj = 0; jj < kBN; ++jj) {
       const float* vr = vt + jj * Dv4;
       float vv[DT];
@@ -257,7 +259,6 @@ __global__ void __launch_bounds__(kWarps * 32) fwd_f32_kernel(FwdArgs a, int til
 #pragma unroll
         for (int t = 0; t < DT; ++t) acc[r][t] = fmaf(p[r], vv[t], acc[r][t]);
     }
-    __syncthreads();  // this tile is consumed
   }
 
   // ---- epilogue ---------------------------------------------------------------------------
@@ -353,6 +354,7 @@ cudaError_t launch_dmax(const FwdArgs& a, cudaStream_t st) {
 
 cudaError_t launch_fwd_f32(const FwdArgs& a, cudaStream_t st) {
   if (a.D <= 64) return launch_dmax<64>(a, st);
+  if (a.D <= 96) return launch_dmax<96>(a, st);
   if (a.D <= 128) return launch_dmax<128>(a, st);
   return launch_dmax<256>(a, st);
 }
