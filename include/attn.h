@@ -31,7 +31,8 @@
  *     attn_get_last_error() reads. The kernel skips the offending unit of work (its outputs
  *     are left as zeros where that is stated below) and never traps or aborts.
  *   - Results are deterministic: the same inputs give bitwise-identical outputs (no atomics
- *     take part in any result).
+ *     take part in any result but those on integers in the attn_cache_ calls, whose order does
+ *     not change it).
  *   - Every function is thread-safe; calls on different streams may overlap.
  *   - No call allocates device memory. The library's own device memory, per device: the status
  *     word, the work counters of attn_fwd's persistent grid (one pair for each of the first 256
@@ -362,7 +363,7 @@ ATTN_API int attn_fwd_sinks(const void* q, const void* k, const void* v,
  *                   shared between rows. Every max_pages * page_size <= 2^30.
  * seq_lens          int32 [B]: tokens of each row, 0 <= seq_lens[b] <= max_pages * page_size.
  * ref_count         int32 [num_pages]: in how many places a page is held (table entries, and whatever
- *                   the caller counts beside them); 0 = free. Below 2^17.
+ *                   the caller counts beside them); 0 = free; at most 2^16.
  * All of these are device arrays. Their contents are checked on the device: what is out of range sets
  * ATTN_ERR_DATA in the status word and is skipped as stated for each call; it is never dereferenced.
  * Tables have at most 8192 rows and 2^29 entries in the calls that change them.
@@ -444,7 +445,7 @@ ATTN_API int attn_cache_fork(const int32_t* page_table, const int32_t* src_rows,
  * earlier tokens of its row has to be copied: copies int32 [B, 2] gets (source, destination) for each
  * row, or (-1, -1), for attn_cache_copy (once per layer whose caches share the table).
  * All or nothing: where fewer pages are free than needed, ATTN_ERR_PAGES is recorded; where a length,
- * an entry or a count is out of range (a held page with count 0 among them), ATTN_ERR_DATA. page_table
+ * an entry or a count is out of range (a held page with count 0, or with fewer than ask for it), ATTN_ERR_DATA. page_table
  * and ref_count are then as before, and copies is all -1.
  */
 ATTN_API int attn_cache_reserve(int32_t* page_table, int32_t* ref_count, const int32_t* seq_lens,

@@ -3,8 +3,8 @@
 The operations (attn_fwd, attn_fwd_masked, attn_fwd_accumulate, attn_sparse_csr,
 attn_sparse_csr_tc, attn_csr_plan_size, attn_csr_plan, attn_sparse_csr_tc_planned, attn_merge,
 attn_fwd_sinks, attn_decode_workspace_size, attn_decode_paged, attn_cache_append, attn_cache_fork,
-attn_cache_reserve, attn_cache_evict, attn_cache_compact, attn_cache_copy, attn_get_last_error) are the C-ABI calls declared in
-``include/attn.h``; the functions here carry the same names and only marshal arguments (tensor
+attn_cache_reserve, attn_cache_evict, attn_cache_compact, attn_cache_copy, attn_get_last_error) are the
+C-ABI calls declared in ``include/attn.h``; the functions here carry the same names and only marshal arguments (tensor
 data pointers, sizes, the current CUDA stream) into them. Every step of the computation runs in the library's CUDA kernels.
 There is no CPU path: if ``libattn.so`` is missing the first call raises.
 
@@ -14,6 +14,7 @@ layouts the header states) and preallocated outputs.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 from typing import Optional
@@ -386,6 +387,20 @@ def _arg(x, name: str, numel: int, dt, dev: int) -> Optional[int]:
     return _ptr(x, name, max(numel, 0), str(dt).replace("torch.", "") if dt is not None else None)
 
 
+def _plain(x):
+    """A number of another library as one that ctypes takes."""
+    if x is None or isinstance(x, (int, float)):
+        return x
+    return operator.index(x) if hasattr(x, "__index__") else float(x)
+
+
+def _call(fn, *args) -> int:
+    try:
+        return fn(*args)
+    except ctypes.ArgumentError:
+        return fn(*[_plain(x) for x in args])
+
+
 def _on(stream, dev: int) -> Optional[int]:
     """The stream to launch on, as _stream gives it."""
     if stream is None and dev >= 0:
@@ -401,7 +416,8 @@ def attn_fwd_sinks(q, k, v, *, cu_seqlens_q=None, cu_seqlens_kv=None, B: int, Sq
     lib, dev = _lib or load_library(), _here()
     nq, nk, _, no, ns = _fwd_sizes(B, Sq, Skv, Nq, Nkv, D, D, layout)
     et, f32, i32 = _DEV["elem"].get(dtype), _DEV["f32"], _DEV["i32"]
-    rc = lib.attn_fwd_sinks(
+    rc = _call(
+        lib.attn_fwd_sinks,
         _arg(q, "q", nq, et, dev), _arg(k, "k", nk, et, dev), _arg(v, "v", nk, et, dev),
         None if cu_seqlens_q is None else _arg(cu_seqlens_q, "cu_seqlens_q", B, i32, dev),
         None if cu_seqlens_kv is None else _arg(cu_seqlens_kv, "cu_seqlens_kv", B, i32, dev), B, Sq, Skv, Nq, Nkv, D,
@@ -454,7 +470,8 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, seq_lens, *, B: int, Nq: 
         ws_bytes = attn_decode_workspace_size(Nq=Nq, Nkv=Nkv, D=D, dtype=dtype)
     else:
         ws_bytes = workspace.numel()
-    rc = lib.attn_decode_paged(
+    rc = _call(
+        lib.attn_decode_paged,
         _arg(q, "q", nq, et, dev), _pool(k_cache, "k_cache", num_pages, pe, page_stride, et, dev),
         _pool(v_cache, "v_cache", num_pages, pe, page_stride, et, dev),
         _arg(page_table, "page_table", B * max_pages, i32, dev), _arg(seq_lens, "seq_lens", B, i32, dev), B, Nq, Nkv, D,
@@ -474,7 +491,8 @@ def attn_cache_append(k, v, page_table, seq_lens, k_cache, v_cache, *, cu_seqlen
     lib, dev = _lib or load_library(), _here()
     et, i32 = _DEV["elem"].get(dtype), _DEV["i32"]
     nk, pe = T * Nkv * D, page_size * Nkv * D
-    rc = lib.attn_cache_append(
+    rc = _call(
+        lib.attn_cache_append,
         _arg(k, "k", nk, et, dev), _arg(v, "v", nk, et, dev), _arg(page_table, "page_table", B * max_pages, i32, dev),
         _arg(seq_lens, "seq_lens", B, i32, dev),
         None if cu_seqlens is None else _arg(cu_seqlens, "cu_seqlens", B, i32, dev), T, B, Nkv, D, num_pages, page_size,
@@ -491,7 +509,8 @@ def attn_cache_fork(page_table, src_rows, ref_count, page_table_out, ref_count_o
     in include/attn.h). The outputs may be the inputs."""
     lib, dev = _lib or load_library(), _here()
     i32 = _DEV["i32"]
-    rc = lib.attn_cache_fork(
+    rc = _call(
+        lib.attn_cache_fork,
         _arg(page_table, "page_table", rows_in * max_pages, i32, dev), _arg(src_rows, "src_rows", rows_out, i32, dev),
         _arg(ref_count, "ref_count", num_pages, i32, dev),
         None if seq_lens is None else _arg(seq_lens, "seq_lens", rows_in, i32, dev), rows_in, rows_out, max_pages,
@@ -508,7 +527,8 @@ def attn_cache_reserve(page_table, ref_count, seq_lens, new_tokens, copies, *, B
     include/attn.h). `new_tokens` may be None (one per row)."""
     lib, dev = _lib or load_library(), _here()
     i32 = _DEV["i32"]
-    rc = lib.attn_cache_reserve(
+    rc = _call(
+        lib.attn_cache_reserve,
         _arg(page_table, "page_table", B * max_pages, i32, dev), _arg(ref_count, "ref_count", num_pages, i32, dev),
         _arg(seq_lens, "seq_lens", B, i32, dev),
         None if new_tokens is None else _arg(new_tokens, "new_tokens", B, i32, dev), B, max_pages, num_pages, page_size,
@@ -523,7 +543,8 @@ def attn_cache_evict(page_table, ref_count, seq_lens, *, B: int, max_pages: int,
     include/attn.h)."""
     lib, dev = _lib or load_library(), _here()
     i32 = _DEV["i32"]
-    rc = lib.attn_cache_evict(
+    rc = _call(
+        lib.attn_cache_evict,
         _arg(page_table, "page_table", B * max_pages, i32, dev), _arg(ref_count, "ref_count", num_pages, i32, dev),
         _arg(seq_lens, "seq_lens", B, i32, dev), B, max_pages, num_pages, page_size, window_tokens, sink_tokens,
         _on(stream, dev))
@@ -537,7 +558,8 @@ def attn_cache_compact(page_table, ref_count, page_table_out, ref_count_out, pag
     include/attn.h). page_table_out and ref_count_out may be the inputs."""
     lib, dev = _lib or load_library(), _here()
     i32 = _DEV["i32"]
-    rc = lib.attn_cache_compact(
+    rc = _call(
+        lib.attn_cache_compact,
         _arg(page_table, "page_table", rows * max_pages, i32, dev), _arg(ref_count, "ref_count", num_pages, i32, dev),
         rows, max_pages, num_pages, _arg(page_table_out, "page_table_out", rows * max_pages, i32, dev),
         _arg(ref_count_out, "ref_count_out", num_pages, i32, dev), _arg(page_map, "page_map", num_pages, i32, dev),
@@ -553,9 +575,10 @@ def attn_cache_copy(k_cache, v_cache, copies, *, n_copies: int, num_pages: int, 
     ``attn_cache_copy`` in include/attn.h)."""
     lib, dev = _lib or load_library(), _here()
     et = _DEV["elem"].get(dtype)
-    rc = lib.attn_cache_copy(
-        _arg(copies, "copies", 2 * n_copies, _DEV["i32"], dev), n_copies, num_pages, page_elems, page_stride, dtype,
-        _pool(k_cache, "k_cache", num_pages, page_elems, page_stride, et, dev),
+    rc = _call(
+        lib.attn_cache_copy,
+        _arg(copies, "copies", 2 * n_copies, _DEV["i32"], dev), n_copies, num_pages, page_elems,
+        page_stride, dtype, _pool(k_cache, "k_cache", num_pages, page_elems, page_stride, et, dev),
         _pool(v_cache, "v_cache", num_pages, page_elems, page_stride, et, dev), _on(stream, dev))
     if rc:
         _check(rc, "attn_cache_copy")

@@ -206,13 +206,14 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkArgs a, int cols
 // the same call the first of them, in slot order, keeps it. Nothing is changed unless enough pages
 // are free.
 //
-// The counts themselves carry the bookkeeping between the passes (all counts are below 2^17 and there
+// The counts themselves carry the bookkeeping between the passes (a count is at most kMaxCount and there
 // are at most 8192 slots of one page, one per row): every asking slot takes 2^17 off its shared page's
 // count, which makes it negative and keeps both the count and the number k of askers readable; where
 // k is the count, the slots replace it by the smallest of -2^31 + slot, below every such value.
 constexpr int kResThreads = 1024;
 constexpr int kResWarps = kResThreads / 32;
 constexpr int kAsk = 1 << 17;
+constexpr int kMaxCount = 1 << 16;
 constexpr int kOwned = -(1 << 30);  // below: the keeper's slot; kOwned and above, negative: asked for
 
 struct ResSmem {
@@ -312,21 +313,31 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
   Slot mine{0, false, nullptr};
   if (tid < slots) mine = find(tid);
   auto slot_at = [&](int x) -> Slot { return x == tid ? mine : find(x); };
+  // 0: every entry is a page or none, and every page has a count (one that is held with a count of 0
+  // would be handed out a second time)
+  bool mine_shared = false;
+  for (int x = tid; x < slots; x += kResThreads) {
+    const int page = *slot_at(x).e;
+    if (page < 0) continue;
+    const int v = page < a.num_pages ? a.ref[page] : 0;
+    if (v < 1 || v > kMaxCount) s.bad = 1;
+    if (x == tid) mine_shared = v > 1;
+  }
+  __syncthreads();
+  if (s.bad) {
+    if (tid == 0) report(a.status, ATTN_ERR_DATA);
+    return;
+  }
   // 1: every slot of a shared page asks for it
   for (int x = tid; x < slots; x += kResThreads) {
     const int page = *slot_at(x).e;
-    if (page >= a.num_pages) s.bad = 1;
-    else if (page >= 0 && a.ref[page] != 1) {
-      // a page that is held has a count; 0 here would be handed out a second time
-      if (a.ref[page] == 0) s.bad = 1;
-      else atomicSub(a.ref + page, kAsk);
-    }
+    if (page >= 0 && (x == tid ? mine_shared : *(volatile int32_t*)(a.ref + page) != 1)) atomicSub(a.ref + page, kAsk);
   }
   __syncthreads();
   // 2: where all holders ask, the first slot owns the page
   for (int x = tid; x < slots; x += kResThreads) {
     const int page = *slot_at(x).e;
-    if (page < 0 || page >= a.num_pages) continue;
+    if (page < 0) continue;
     const int v = *(volatile int32_t*)(a.ref + page);
     if (v >= 0) continue;
     const int k = (-v + kAsk - 1) / kAsk;
@@ -336,7 +347,6 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
   __syncthreads();
   auto needs = [&](int x, int page) -> bool {  // slot x needs a free page
     if (page < 0) return true;
-    if (page >= a.num_pages) return false;
     const int v = a.ref[page];
     return v < 0 && v != INT32_MIN + x;
   };
@@ -369,12 +379,12 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
     // undo: an owned page's count is the number of slots that ask for it
     for (int x = tid; x < slots; x += kResThreads) {
       const int page = *slot_at(x).e;
-      if (page >= 0 && page < a.num_pages && a.ref[page] == INT32_MIN + x) a.ref[page] = INT32_MIN;
+      if (page >= 0 && a.ref[page] == INT32_MIN + x) a.ref[page] = INT32_MIN;
     }
     __syncthreads();
     for (int x = tid; x < slots; x += kResThreads) {
       const int page = *slot_at(x).e;
-      if (page < 0 || page >= a.num_pages) continue;
+      if (page < 0) continue;
       const int v = *(volatile int32_t*)(a.ref + page);
       if (v < kOwned) atomicAdd(a.ref + page, 1);
       else if (v < 0) atomicAdd(a.ref + page, kAsk);
@@ -382,7 +392,7 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
     __syncthreads();
     for (int x = tid; x < slots; x += kResThreads) {
       const int page = *slot_at(x).e;
-      if (page >= 0 && page < a.num_pages && a.ref[page] < kOwned) atomicAnd(a.ref + page, INT32_MAX);
+      if (page >= 0 && a.ref[page] < kOwned) atomicAnd(a.ref + page, INT32_MAX);
     }
     if (tid == 0) report(a.status, s.bad ? ATTN_ERR_DATA : ATTN_ERR_PAGES);
     return;

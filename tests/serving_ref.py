@@ -120,7 +120,7 @@ def reserve(table, ref, lens, new, page_size):
         p = table[b][i]
         if p >= num_pages:
             raise Refused("data")
-        if p >= 0 and ref[p] == 0:
+        if p >= 0 and not 1 <= ref[p] <= 1 << 16:
             raise Refused("data")
         if p >= 0 and ref[p] > 1:
             asking.setdefault(p, []).append((b, i))

@@ -223,6 +223,9 @@ def test_reserve_bad_data_changes_nothing():
     _reserve([[0, -1], [2, -1]], ref, [5, 2], [1, 1], 4)   # a held page that counts as free
     _reserve([[0, -1]] * 3, [2, 0, 0, 0], [3] * 3, [1] * 3, 4)  # more holders than the count
     _reserve([[0, -1]] * 2 + [[-1, 7]], [2, 0, 0, 0], [3, 3, 5], [1] * 3, 4)  # data error beside shared pages
+    for count in (1 << 16, (1 << 16) + 1, 1 << 17, (1 << 17) + 5, 2 ** 31 - 1, -1, -5, -(1 << 16)):
+        _reserve([[0, -1]] * 2, [count, 0, 0, 0], [3, 3], [1] * 2, 4)   # the largest count, and what is none
+        _reserve([[0, -1]] * 2, [count, 0, 0, 0], [3, 3], [1, 0], 4)
 
 
 # ---- compact and copy ------------------------------------------------------------------------------

@@ -176,6 +176,11 @@ def test_binding_refuses_wrong_tensors(lib, on_cuda0):
     with pytest.raises(sdpa.AttnError):
         call(workspace=FakeCuda(ws - 1, torch.uint8))
 
+    # sizes and scales of numpy are numbers too (refused by the library here, after the binding took them)
+    import numpy as np
+    with pytest.raises(sdpa.AttnError, match="invalid"):
+        call(B=np.int64(B), Nq=np.int32(Nq), scale=np.float32(0.0))
+
     class Half:
         """A view [num_pages, ...] of every second page of a pool, on a machine without a GPU."""
         is_cuda, dtype, device = True, BF, torch.device("cuda", 0)
