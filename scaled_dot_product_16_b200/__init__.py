@@ -4,9 +4,9 @@ The operations (attn_fwd, attn_fwd_masked, attn_fwd_accumulate, attn_sparse_csr,
 attn_sparse_csr_tc, attn_csr_plan_size, attn_csr_plan, attn_sparse_csr_tc_planned, attn_merge,
 attn_fwd_sinks, attn_decode_workspace_size, attn_decode_paged, attn_cache_append, attn_cache_fork,
 attn_cache_reserve, attn_cache_evict, attn_cache_compact, attn_cache_copy, attn_get_last_error) are the
-C-ABI calls declared in ``include/attn.h``; the functions here carry the same names and only marshal arguments (tensor
-data pointers, sizes, the current CUDA stream) into them. Every step of the computation runs in the library's CUDA kernels.
-There is no CPU path: if ``libattn.so`` is missing the first call raises.
+C-ABI calls declared in ``include/attn.h``; the functions here carry the same names and only marshal
+arguments (tensor data pointers, sizes, the current CUDA stream) into them. Every step of the
+computation runs in the library's CUDA kernels. There is no CPU path: if ``libattn.so`` is missing the first call raises.
 
 PyTorch is used for device memory and streams only: pass CUDA tensors (contiguous, in the
 layouts the header states) and preallocated outputs.
