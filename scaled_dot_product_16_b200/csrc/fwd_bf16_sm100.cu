@@ -792,7 +792,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l = 0.f;
       bool ok = true;
       if (q == 0 || has1) {
-        for (int j = j0; j < n; ++j) {
+        int jb = j0;
+        if (EXT == 3 && !kOwnP && ns == 1 && jlo > 0 && a.sinks <= 32 && n > 0) {
+          // Up to 32 sinks in a tile apart from every row's window: 32 of its columns are read, with no
+          // maximum to compare with and no O to rescale (171 -> 167 us for the packed case; MMAs of 32 keys
+          // for this tile too: 173, the issuing thread's loop is longer then).
+          jb = 1;
+          ok = __all_sync(0xffffffffu, wait_bar(bar_addr(&bars->s_full[q]), sfc & 1, abort, a.status));
+          ++sfc;
+          tc_fence_after();
+          float s[32];
+          tmem_ld32f(S, s);
+          tmem_wait_ld();
+          float tmax = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (c >= a.sinks) s[c] = -INFINITY;
+            tmax = fmaxf(tmax, s[c]);
+          }
+          mraw = tmax;
+          m = tmax * scale_log2;
+          const float muse = m == -INFINITY ? 0.f : m;
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float p0 = ex2(fmaf(s[c], scale_log2, -muse)), p1 = ex2(fmaf(s[c + 1], scale_log2, -muse));
+            l += p0 + p1;
+            pk[c >> 1] = pack16x2<F16>(p0, p1);
+            pk[16 + (c >> 1)] = 0u;
+          }
+          tmem_st32(P, pk);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = 0u;
+          tmem_st32(P + 32, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_addr(&bars->p_ready[q]));
+        }
+        for (int j = jb; ok && j < n; ++j) {
           if (EXT == 3 && q == 1 && j == ns && j < s1) j = s1;  // tiles before Q1's own window
           ok = __all_sync(0xffffffffu, wait_bar(bar_addr(&bars->s_full[q]), sfc & 1, abort, a.status));
           ++sfc;

@@ -74,6 +74,30 @@ def test_varlen_with_longer_keys():
     _check(a, 130, 20)
 
 
+@pytest.mark.parametrize("dtype", [BF, F16], ids=IDS)
+@pytest.mark.parametrize("sinks", [1, 2, 31, 32, 33])
+@pytest.mark.parametrize("gain", [0.0, 1.0, -1.0, 30.0, -30.0])
+def test_few_sinks_apart_from_the_window(dtype, sinks, gain):
+    """A tile that holds only some sinks, whose scores lie at, above or far below those of the window (the row's
+    maximum moves after it or never); keys of that tile behind the sinks are NaN and are not seen."""
+    inp = W.varlen_tnd([700, 300, 1100], 4, 2, 128, causal=False, dtype=dtype, seed=sinks, cfg=79)
+    for b in range(3):
+        t = int(inp.cu_kv[b])
+        q = inp.q[t:t + 256].float().mean((0, 1))
+        inp.k[t:t + sinks] = (gain * (inp.k[t:t + sinks].float().abs() + 0.1) * torch.sign(q)).to(dtype)
+    _check(inp, 100, sinks)
+    x = _run(inp, 100, sinks)
+    for b in range(3):
+        t = int(inp.cu_kv[b])
+        rows = inp.k[t + sinks:t + 120].clone()
+        inp.k[t + sinks:t + 120] = float("nan")
+        y = _run(inp, 100, sinks)
+        inp.k[t + sinks:t + 120] = rows
+        # rows whose window begins behind the NaN
+        for u, v in zip(x, y):
+            assert torch.equal(u[t + 230:t + 300], v[t + 230:t + 300])
+
+
 @pytest.mark.parametrize("D", [1, 33, 80, 256])
 def test_f32_head_sizes(D):
     _check(W.dense_bhsd(1, 2, 150, D, causal=False, dtype=F32, seed=D, cfg=76), 40, 3)
