@@ -222,8 +222,11 @@ __device__ __forceinline__ void finish_unit(const DecodeArgs& a, const Cursor<TI
     if (whole) {
       write(r, d, m, l, o);
     } else {
+      if constexpr (V == 4)
+        __stcg(reinterpret_cast<float4*>(slot + r * D + d), make_float4(o[0], o[1], o[2], o[3]));
+      else
 #pragma unroll
-      for (int i = 0; i < V; ++i) __stcg(slot + r * D + d + i, o[i]);
+        for (int i = 0; i < V; ++i) __stcg(slot + r * D + d + i, o[i]);
       if (d == 0) __stcg(reinterpret_cast<float2*>(slot + a.rows * D) + r, make_float2(m, l));
     }
   }
@@ -238,13 +241,16 @@ __device__ __forceinline__ void finish_unit(const DecodeArgs& a, const Cursor<TI
   // whether this block is the last of n to arrive at a counter
   auto last_of = [&](unsigned* ctr, int n) -> bool {
     if (n == 1) return true;
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) s->last = atomicInc(ctr, (unsigned)n - 1) == (unsigned)n - 1;
+    if (threadIdx.x == 0) {
+      // releases the block's writes before its barrier and acquires those of the blocks that came earlier (fences
+      // in every thread instead took 34 and not 32.5 us for two sequences of 131,072 and 81,007 keys)
+      unsigned was;
+      asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(was) : "l"(ctr), "r"((unsigned)n - 1) : "memory");
+      s->last = was == (unsigned)n - 1;
+    }
     __syncthreads();
-    const bool last = s->last;
-    __threadfence();
-    return last;
+    return s->last;
   };
   // joins n parts i0, i0 + step, ...; the result replaces part i0, or is the unit's
   auto join = [&](int i0, int n, int step, bool final) {
@@ -781,11 +787,18 @@ __global__ void __launch_bounds__(kThreads) decode_f32_kernel(DecodeArgs a, floa
     const int hk = c.u / a.groups, g0 = (c.u - hk * a.groups) * R;
     const int n_rows = min(R, G - g0);
     const float* Q = static_cast<const float*>(a.q) + ((int64_t)c.b * a.Nq + (int64_t)hk * G + g0) * a.D;
-    __syncwarp();
-    for (int x = lane; x < R * DM; x += 32) {
-      const int r = x / DM, d = x % DM;
-      s_q[x] = r < n_rows && d < a.D ? __ldg(Q + r * a.D + d) : 0.f;
+    // every load of the heads before the first store, or the unit begins with several trips to memory (61 MB of
+    // keys and values in 32 units: 25.3 -> 23.4 us); Q is 16-byte aligned and a.D a multiple of 4
+    float4 q[R * C::kChunks / 32];
+#pragma unroll
+    for (int i = 0; i < R * C::kChunks / 32; ++i) {
+      const int x = lane + 32 * i, r = x / C::kChunks, d = x % C::kChunks * 4;
+      q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < n_rows && d < a.D) q[i] = __ldg(reinterpret_cast<const float4*>(Q + r * a.D + d));
     }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < R * C::kChunks / 32; ++i) reinterpret_cast<float4*>(s_q)[lane + 32 * i] = q[i];
     __syncwarp();
     float o[R][4], m[RG], l[RG];
 #pragma unroll
