@@ -12,9 +12,11 @@
 // form: the running maximum and sum are rescaled when the maximum grows. attn_fwd_sinks leaves out
 // the key tiles between the first keys and the block's window.
 //
-// The tiles come by asynchronous copies (16 bytes at a time where rows allow it), the next one while
-// the current one is multiplied: with plain loads a block of few key tiles spent most of its time
-// waiting for them (2 x 4 x 333 x 80, window 128: 121 us, now 28). Rows are padded to whole 16-byte chunks, so that
+// The tiles come by asynchronous copies, the next one while the current one is multiplied: with plain
+// loads a block of few key tiles spent most of its time waiting for them (2 x 4 x 333 x 80, window 128:
+// 121 us, now 25). Where rows are whole 16-byte chunks a row is one bulk copy, issued by four lanes of
+// each warp: per-thread copies took every warp 2,000 of a tile's 7,000 cycles to issue (28 us; all rows
+// from one warp: 33). Rows are padded to whole 16-byte chunks, so that
 // queries and keys are read four columns at a time, and the weights four rows at a time: the loop is
 // bound by shared-memory reads otherwise. The order of every sum is that of one column, and one key,
 // after the other.
@@ -22,6 +24,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "sm100.cuh"
 
 namespace sdpa {
 namespace {
@@ -33,28 +36,33 @@ constexpr int kBN = 32;       // keys per tile
 constexpr int kWarps = 8;
 constexpr int kRowsPerWarp = kBM / kWarps;
 
-// 4 or 16 bytes to shared memory, or zeros where !ok (src is then not read)
-template <int BYTES>
+using namespace sm100;
+
+constexpr uint64_t kWaitNs = 1000ull * 1000ull * 1000ull;  // bound on the wait for a tile
+
+// 4 bytes to shared memory, or a zero where !ok (src is then not read)
 __device__ __forceinline__ void stage(float* dst, const float* src, bool ok) {
-  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(ok ? 16 : 0) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(ok ? 4 : 0) : "memory");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 4 : 0) : "memory");
 }
 
 // kBN rows of D columns into rows of `ld` floats whose columns up to a multiple of 4 become zeros; rows
 // from `rows` on become zeros.
-template <int BYTES>
 __device__ __forceinline__ void stage_tile(float* dst, int ld, const float* src, int64_t stride, int rows, int D) {
-  constexpr int N = BYTES / 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int D4 = (D + 3) / 4 * 4;
   for (int r = warp; r < kBN; r += kWarps)
-    for (int c = lane * N; c < D4; c += 32 * N) {
+    for (int c = lane; c < D4; c += 32) {
       const bool ok = r < rows && c < D;
-      stage<BYTES>(dst + r * ld + c, ok ? src + r * stride + c : src, ok);
+      stage(dst + r * ld + c, ok ? src + r * stride + c : src, ok);
     }
+}
+
+__device__ __forceinline__ bool wait_tile(uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 20000))
+    if (globaltimer_ns() - t0 > kWaitNs) return false;
+  return true;
 }
 
 // Three blocks an SM at head sizes up to 64, whose tiles leave the shared memory for it (4 x 16 x 1,024, window
@@ -70,6 +78,7 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kerne
   float* sK = sP + kWarps * kRowsPerWarp * kBN;  // [2][kBN][ldk]
   float* sV = sK + 2 * kBN * ldk;         // [2][kBN][Dv4]
   __shared__ int s_info[4];
+  __shared__ __align__(8) uint64_t s_full[2];  // the tile of each buffer has come (16-byte rows)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Blocks start in the order of their index: the heads of a query tile side by side, and the last tiles of
@@ -102,6 +111,9 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kerne
       }
     }
     if (lane == 0) {
+      mbar_init(smem_u32(&s_full[0]), 1);
+      mbar_init(smem_u32(&s_full[1]), 1);
+      fence_mbar_init();
       s_info[0] = ok;
       s_info[1] = b;
       s_info[2] = t;
@@ -156,12 +168,27 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kerne
   const int64_t k_stride = a.layout == ATTN_BHSD ? D : (int64_t)a.Nkv * D;
   const int64_t v_stride = a.layout == ATTN_BHSD ? Dv : (int64_t)a.Nkv * Dv;
   auto fetch = [&](int j0, int buf) {  // the key tile at j0, or nothing
-    if (vec) {
-      stage_tile<16>(sK + buf * kBN * ldk, ldk, K + kvoff(j0), k_stride, sk - j0, D);
-      stage_tile<16>(sV + buf * kBN * Dv4, Dv4, V + voff(j0), v_stride, sk - j0, Dv);
+    float* kt = sK + buf * kBN * ldk;
+    float* vt = sV + buf * kBN * Dv4;
+    if (!vec) {
+      stage_tile(kt, ldk, K + kvoff(j0), k_stride, sk - j0, D);
+      stage_tile(vt, Dv4, V + voff(j0), v_stride, sk - j0, Dv);
     } else {
-      stage_tile<4>(sK + buf * kBN * ldk, ldk, K + kvoff(j0), k_stride, sk - j0, D);
-      stage_tile<4>(sV + buf * kBN * Dv4, Dv4, V + voff(j0), v_stride, sk - j0, Dv);
+      // Four lanes of each warp, a row each. Value rows behind the last key become zeros: their weights are
+      // 0, but what lies there may be anything. (Keys there are not looked at.)
+      constexpr int kRows = kBN / kWarps;
+      const int rows = min(kBN, sk - j0), r = warp * kRows + lane;
+      const uint32_t bar = smem_u32(&s_full[buf]);
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, rows * (D + Dv) * 4);
+      if (lane < kRows) {
+        if (r < rows) {
+          bulk_load(smem_u32(kt + r * ldk), K + kvoff(j0) + r * k_stride, D * 4, bar);
+          bulk_load(smem_u32(vt + r * Dv4), V + voff(j0) + r * v_stride, Dv * 4, bar);
+        } else {
+          for (int c = 0; c < Dv; c += 4) *reinterpret_cast<float4*>(vt + r * Dv4 + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+      __syncwarp();
     }
   };
 
@@ -188,13 +215,19 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kerne
   }
 
   auto after = [&](int j0) { return j0 + kBN == sink_end ? kv_begin : j0 + kBN; };
-  int buf = 0;
+  int buf = 0, it = 0;
   const int j_first = sink_end > 0 ? 0 : kv_begin;
   if (j_first < kv_end) fetch(j_first, 0);
   asm volatile("cp.async.commit_group;" ::: "memory");
-  for (int j0 = j_first; j0 < kv_end; j0 = after(j0), buf ^= 1) {
+  for (int j0 = j_first; j0 < kv_end; j0 = after(j0), buf ^= 1, ++it) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();  // this tile is there (and Q, on the first pass), and the last one is consumed
+    const bool come = !vec || wait_tile(smem_u32(&s_full[buf]), (it >> 1) & 1);
+    // this tile is there (and Q, on the first pass), and the last one is consumed
+    if (__syncthreads_or(!come)) {
+      if (threadIdx.x == 0) report(a.status, ATTN_ERR_TIMEOUT);
+      wait_tile(smem_u32(&s_full[buf]), (it >> 1) & 1);  // no copy outlives the block
+      return;
+    }
     if (after(j0) < kv_end) fetch(after(j0), buf ^ 1);
     asm volatile("cp.async.commit_group;" ::: "memory");
 
