@@ -14,9 +14,9 @@
 //
 // The tiles come by asynchronous copies, the next one while the current one is multiplied: with plain
 // loads a block of few key tiles spent most of its time waiting for them (2 x 4 x 333 x 80, window 128:
-// 121 us, now 25). Where rows are whole 16-byte chunks a row is one bulk copy, issued by four lanes of
+// 121 us, now 22). Where rows are whole 16-byte chunks a row is one bulk copy, issued by four lanes of
 // each warp: per-thread copies took every warp 2,000 of a tile's 7,000 cycles to issue (28 us; all rows
-// from one warp: 33). Rows are padded to whole 16-byte chunks, so that
+// from one warp: 33), the queries with the first tile (25 -> 22 us). Rows are padded to whole 16-byte chunks, so that
 // queries and keys are read four columns at a time, and the weights four rows at a time: the loop is
 // bound by shared-memory reads otherwise. The order of every sum is that of one column, and one key,
 // after the other.
@@ -163,24 +163,26 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kerne
   const int row0 = qt * kBM;
   const int nrows = min(kBM, sq - row0);
   // stage Q (rows past the sequence end are zero-filled)
-  for (int r = warp; r < kBM; r += kWarps)
-    for (int d = lane; d < D4; d += 32) sQ[r * D4 + d] = r < nrows && d < D ? Q[qoff(row0 + r) + d] : 0.f;
+  if (!vec)
+    for (int r = warp; r < kBM; r += kWarps)
+      for (int d = lane; d < D4; d += 32) sQ[r * D4 + d] = r < nrows && d < D ? Q[qoff(row0 + r) + d] : 0.f;
+  constexpr int kLaneRows = kBN / kWarps;  // vec: the first lanes of each warp copy a row each
+  static_assert(kBN == kBM, "rows of a tile");
   const int64_t k_stride = a.layout == ATTN_BHSD ? D : (int64_t)a.Nkv * D;
   const int64_t v_stride = a.layout == ATTN_BHSD ? Dv : (int64_t)a.Nkv * Dv;
-  auto fetch = [&](int j0, int buf) {  // the key tile at j0, or nothing
+  auto fetch = [&](int j0, int buf, int bytes) {  // the key tile at j0; `bytes` more come to its barrier
     float* kt = sK + buf * kBN * ldk;
     float* vt = sV + buf * kBN * Dv4;
     if (!vec) {
       stage_tile(kt, ldk, K + kvoff(j0), k_stride, sk - j0, D);
       stage_tile(vt, Dv4, V + voff(j0), v_stride, sk - j0, Dv);
     } else {
-      // Four lanes of each warp, a row each. Value rows behind the last key become zeros: their weights are
-      // 0, but what lies there may be anything. (Keys there are not looked at.)
-      constexpr int kRows = kBN / kWarps;
-      const int rows = min(kBN, sk - j0), r = warp * kRows + lane;
+      // Value rows behind the last key become zeros: their weights are 0, but what lies there may be
+      // anything. (Keys there are not looked at.)
+      const int rows = min(kBN, sk - j0), r = warp * kLaneRows + lane;
       const uint32_t bar = smem_u32(&s_full[buf]);
-      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, rows * (D + Dv) * 4);
-      if (lane < kRows) {
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, rows * (D + Dv) * 4 + bytes);
+      if (lane < kLaneRows) {
         if (r < rows) {
           bulk_load(smem_u32(kt + r * ldk), K + kvoff(j0) + r * k_stride, D * 4, bar);
           bulk_load(smem_u32(vt + r * Dv4), V + voff(j0) + r * v_stride, Dv * 4, bar);
@@ -217,7 +219,17 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kerne
   auto after = [&](int j0) { return j0 + kBN == sink_end ? kv_begin : j0 + kBN; };
   int buf = 0, it = 0;
   const int j_first = sink_end > 0 ? 0 : kv_begin;
-  if (j_first < kv_end) fetch(j_first, 0);
+  if (j_first < kv_end) {
+    if (vec && lane < kLaneRows) {  // Q with the first tile
+      const int r = warp * kLaneRows + lane;
+      if (r < nrows)
+        bulk_load(smem_u32(sQ + r * D4), Q + qoff(row0 + r), D * 4, smem_u32(&s_full[0]));
+      else
+        for (int c = 0; c < D; c += 4) *reinterpret_cast<float4*>(sQ + r * D4 + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncwarp();
+    fetch(j_first, 0, nrows * D * 4);
+  }
   asm volatile("cp.async.commit_group;" ::: "memory");
   for (int j0 = j_first; j0 < kv_end; j0 = after(j0), buf ^= 1, ++it) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -228,7 +240,7 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kerne
       wait_tile(smem_u32(&s_full[buf]), (it >> 1) & 1);  // no copy outlives the block
       return;
     }
-    if (after(j0) < kv_end) fetch(after(j0), buf ^ 1);
+    if (after(j0) < kv_end) fetch(after(j0), buf ^ 1, 0);
     asm volatile("cp.async.commit_group;" ::: "memory");
 
     // scores: lane = key j0 + lane, one value per row of this warp
@@ -389,8 +401,8 @@ cudaError_t launch_dmax(const FwdArgs& a, cudaStream_t st) {
   if (gx <= 0) return cudaSuccess;
   if (gx * a.Nq > 0x7fffffff) return cudaErrorInvalidConfiguration;  // 2^36 query rows and more
   const unsigned grid = (unsigned)(gx * a.Nq);
-  const int vec = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15u) == 0 && a.D % 4 == 0 &&
-                  a.Dv % 4 == 0;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
+  const int vec = (all & 15u) == 0 && a.D % 4 == 0 && a.Dv % 4 == 0;
   fwd_f32_kernel<DMAX><<<grid, kWarps * 32, smem, st>>>(a, tiles_per_seq, vec);
   return cudaGetLastError();
 }

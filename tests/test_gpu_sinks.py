@@ -204,8 +204,8 @@ def test_bad_lengths_are_reported():
 
 @pytest.mark.parametrize("D", [4, 64, 100, 256])
 def test_f32_tiles_at_any_alignment(D):
-    """Keys and values whose rows are whole 16-byte chunks come by another kind of copy than those at an odd
-    address: the results are the same bits. The keys behind a head's last one are the next head's, here NaN."""
+    """Rows of whole 16-byte chunks come by another kind of copy than those at an odd address: the results
+    are the same bits. The keys behind a head's last one are the next head's, here NaN."""
     inp = W.dense_bhsd(1, 3, 75, D, causal=False, dtype=F32, seed=D, cfg=82, Skv=109)
     inp.k[:, 1], inp.v[:, 1] = float("nan"), float("nan")
     q, k, v, cq, ck = G.to_dev(inp)
@@ -217,6 +217,6 @@ def test_f32_tiles_at_any_alignment(D):
         room[1:] = t.flatten()
         return room[1:].view(t.shape)
 
-    for a, b in ((shifted(k), v), (k, shifted(v)), (shifted(k), shifted(v))):
-        for x, y in zip(want, _run(inp, 50, 5, dev=(q, a, b, cq, ck))):
+    for c, a, b in ((q, shifted(k), v), (q, k, shifted(v)), (shifted(q), k, v), (shifted(q), shifted(k), shifted(v))):
+        for x, y in zip(want, _run(inp, 50, 5, dev=(c, a, b, cq, ck))):
             assert torch.equal(x.nan_to_num(nan=7.0), y.nan_to_num(nan=7.0))
