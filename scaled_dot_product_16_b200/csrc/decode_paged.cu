@@ -509,7 +509,12 @@ struct SwzPair {  // two rows at four chunks in a row
 // with m16n8k16 products and fp32 sums. Keys are the rows of the first product, so a group of up to
 // 8 query heads costs 8 columns and not 16. The blocks' warps meet only at the end of a unit.
 // P in 16 bits: fp16 keeps 2^-11 of a weight; bf16 would keep 2^-8, so it goes in as two terms, p and
-// what rounding left of it (2^-16): the second product is free, the call waits for HBM.
+// what rounding left of it (2^-16): the second product is free, the call waits for HBM. A weight relative to
+// the largest one may be tiny and still count, as there may be many like it behind one key that takes most of
+// the weight. fp16 has no normal numbers below 2^-14, so its weights are kept times 2^15 until the unit ends: the
+// largest is 2^15, and normal ones reach down to 2^-29 of it. (Kept as they are, keys below 2^-25 of their warp's
+// largest one counted in the sum of e^(s - m) and not in that of e^(s - m) v. Windows of 4,096 keys over 16
+// sequences take 46.4 us either way.)
 // tcgen05 would pad the 1 to 16 rows of queries to 64 or 128 and fill its operands through the same
 // shared memory; at most 16 rows of heads, mma.sync is far from its limit here.
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -573,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) decode_tc_kernel(De
   using C = TcCfg<D, NB>;
   constexpr bool kF16 = sizeof(T) == 2 && std::is_same<T, __half>::value;
   constexpr int kTile = C::kTile, kMb = C::kMb;
+  constexpr float kBias = kF16 ? 15.f : 0.f, kUnbias = kF16 ? 0x1p-15f : 1.f;  // weights are kept times 2^kBias
   extern __shared__ __align__(128) uint8_t tc_smem[];
   __shared__ SchedSmem sched;
   __shared__ unsigned s_seen[kWarps][C::kStages];  // bit r: key r of the stage is visible
@@ -674,15 +680,23 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) decode_tc_kernel(De
             o[b][k][3] *= f1;
           }
         }
-        const float c0 = m[b][0] == -INFINITY ? 0.f : -m[b][0] * scale_log2;
-        const float c1 = m[b][1] == -INFINITY ? 0.f : -m[b][1] * scale_log2;
+        const float u0 = m[b][0] == -INFINITY ? 0.f : m[b][0], u1 = m[b][1] == -INFINITY ? 0.f : m[b][1];
+        const float c0 = -u0 * scale_log2, c1 = -u1 * scale_log2;
 #pragma unroll
         for (int j = 0; j < kMb; ++j) {
           float e[4];
-          e[0] = ex2_approx(fmaf(s[b][j][0], scale_log2, c0));
-          e[1] = ex2_approx(fmaf(s[b][j][1], scale_log2, c1));
-          e[2] = ex2_approx(fmaf(s[b][j][2], scale_log2, c0));
-          e[3] = ex2_approx(fmaf(s[b][j][3], scale_log2, c1));
+          if constexpr (kF16) {
+            // the difference first: rounding scale m may not take a weight above 2^15 (fp16 ends at 65,504)
+            e[0] = ex2_approx(fmaf(s[b][j][0] - u0, scale_log2, kBias));
+            e[1] = ex2_approx(fmaf(s[b][j][1] - u1, scale_log2, kBias));
+            e[2] = ex2_approx(fmaf(s[b][j][2] - u0, scale_log2, kBias));
+            e[3] = ex2_approx(fmaf(s[b][j][3] - u1, scale_log2, kBias));
+          } else {
+            e[0] = ex2_approx(fmaf(s[b][j][0], scale_log2, c0));
+            e[1] = ex2_approx(fmaf(s[b][j][1], scale_log2, c1));
+            e[2] = ex2_approx(fmaf(s[b][j][2], scale_log2, c0));
+            e[3] = ex2_approx(fmaf(s[b][j][3], scale_log2, c1));
+          }
           l[b][0] += e[0] + e[2];
           l[b][1] += e[1] + e[3];
           const uint32_t h0 = pack2<T>(e[0], e[1]), h1 = pack2<T>(e[2], e[3]);
@@ -720,14 +734,14 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) decode_tc_kernel(De
       float* w0 = s_w + (warp * C::kRows + 8 * b + t2) * C::kLd + g;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        w0[16 * k] = o[b][k][0];
-        w0[16 * k + C::kLd] = o[b][k][1];
-        w0[16 * k + 8] = o[b][k][2];
-        w0[16 * k + 8 + C::kLd] = o[b][k][3];
+        w0[16 * k] = o[b][k][0] * kUnbias;
+        w0[16 * k + C::kLd] = o[b][k][1] * kUnbias;
+        w0[16 * k + 8] = o[b][k][2] * kUnbias;
+        w0[16 * k + 8 + C::kLd] = o[b][k][3] * kUnbias;
       }
       if (g == 0) {
-        s_wml[warp * C::kRows + 8 * b + t2] = make_float2(m[b][0], l[b][0]);
-        s_wml[warp * C::kRows + 8 * b + t2 + 1] = make_float2(m[b][1], l[b][1]);
+        s_wml[warp * C::kRows + 8 * b + t2] = make_float2(m[b][0], l[b][0] * kUnbias);
+        s_wml[warp * C::kRows + 8 * b + t2 + 1] = make_float2(m[b][1], l[b][1] * kUnbias);
       }
     }
     __syncthreads();
