@@ -380,7 +380,8 @@ ATTN_API int attn_fwd_sinks(const void* q, const void* k, const void* v,
  * the window may be -1 (attn_cache_evict), and what lies in a page behind the last token, or in
  * positions that are not seen, may hold anything, NaN included.
  * ATTN_BF16 and ATTN_F16 with D = 64 or 128, 16-byte aligned q, caches and page_stride run on the
- * tensor cores (products exact, sums in float32, probabilities kept to 16 bits or more); other head
+ * tensor cores (products exact, sums in float32, probabilities kept to 2^-16 of themselves; those of
+ * ATTN_F16 also to no less than 2^-40 of the largest); other head
  * sizes up to 256, alignments and ATTN_F32 on the CUDA cores in float32. Nq / Nkv may be any integer.
  * workspace  device memory of attn_decode_workspace_size bytes, 16-byte aligned, filled with zeros
  *            once before its first use; every call leaves it ready for the next one, of any sizes that

@@ -508,11 +508,11 @@ struct SwzPair {  // two rows at four chunks in a row
 //   O^T [D x 8 NB heads] += V^T P^T            (V by ldmatrix.trans, P^T from S^T by movmatrix)
 // with m16n8k16 products and fp32 sums. Keys are the rows of the first product, so a group of up to
 // 8 query heads costs 8 columns and not 16. The blocks' warps meet only at the end of a unit.
-// P in 16 bits: fp16 keeps 2^-11 of a weight; bf16 would keep 2^-8, so it goes in as two terms, p and
-// what rounding left of it (2^-16): the second product is free, the call waits for HBM. A weight relative to
+// P in 16 bits would keep 2^-8 (bf16) or 2^-11 (fp16) of a weight, so it goes in as two terms, p and what
+// rounding left of it (2^-16; fp16 2^-22): the second product is free, the call waits for HBM. A weight relative to
 // the largest one may be tiny and still count, as there may be many like it behind one key that takes most of
 // the weight. fp16 has no normal numbers below 2^-14, so its weights are kept times 2^15 until the unit ends: the
-// largest is 2^15, and normal ones reach down to 2^-29 of it. (Kept as they are, keys below 2^-25 of their warp's
+// largest is 2^15, normal ones reach down to 2^-29 of it, and the two terms together end at 2^-40 of it. (Kept as they are, keys below 2^-25 of their warp's
 // largest one counted in the sum of e^(s - m) and not in that of e^(s - m) v. Windows of 4,096 keys over 16
 // sequences take 46.4 us either way.)
 // tcgen05 would pad the 1 to 16 rows of queries to 64 or 128 and fill its operands through the same
@@ -549,6 +549,11 @@ template <typename T>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   T t[2] = {from_f<T>(x), from_f<T>(y)};
   return *reinterpret_cast<uint32_t*>(t);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+  const T* t = reinterpret_cast<const T*>(&x);
+  return make_float2(to_f(t[0]), to_f(t[1]));
 }
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -702,12 +707,9 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) decode_tc_kernel(De
           const uint32_t h0 = pack2<T>(e[0], e[1]), h1 = pack2<T>(e[2], e[3]);
           ph[b][j][0] = transpose8(h0);
           ph[b][j][1] = transpose8(h1);
-          if constexpr (!kF16) {
-            const float2 r0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h0));
-            const float2 r1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&h1));
-            pl[b][j][0] = transpose8(pack2<T>(e[0] - r0.x, e[1] - r0.y));
-            pl[b][j][1] = transpose8(pack2<T>(e[2] - r1.x, e[3] - r1.y));
-          }
+          const float2 r0 = unpack2<T>(h0), r1 = unpack2<T>(h1);
+          pl[b][j][0] = transpose8(pack2<T>(e[0] - r0.x, e[1] - r0.y));
+          pl[b][j][1] = transpose8(pack2<T>(e[2] - r1.x, e[3] - r1.y));
         }
       }
 #pragma unroll
@@ -719,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) decode_tc_kernel(De
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             mma16816<kF16>(o[b][k], vf, ph[b][j][0], ph[b][j][1]);
-            if constexpr (!kF16) mma16816<kF16>(o[b][k], vf, pl[b][j][0], pl[b][j][1]);
+            mma16816<kF16>(o[b][k], vf, pl[b][j][0], pl[b][j][1]);
           }
         }
       }

@@ -86,3 +86,29 @@ def test_the_bound_tells_weights_of_plain_fp16_apart(weight):
         kept = (w * 2.0 ** bias).to(F16).double() * 2.0 ** -bias
         err = ((kept @ v) / w.sum() - ref[0][0, 0]).abs()
         assert bool(torch.all(err <= tol[0, 0])) == good, (bias, float((err / tol[0, 0]).max()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F16, BF, F32], ids=IDS)
+@pytest.mark.parametrize("shift", [0, 1], ids=["aligned", "unaligned"])
+@pytest.mark.parametrize("D,heads", [(64, (4, 1)), (128, (4, 1)), (128, (16, 1))])
+def test_two_values_that_nearly_cancel(D, heads, shift, dtype):
+    """Two keys with nearly the same weight and opposite values: the output is the difference of the weights, so it
+    shows how many bits of them reach the product with V. u = 2^-16 for every type and any alignment."""
+    c = Case([2] * 40, *heads, D, dtype, seed=3)
+    c.q = (c.q.float() * 0.05).to(dtype)
+    first = c.table[:, 0].long()
+    c.v[first, 1] = -c.v[first, 0]
+    args = c.dev()
+    if shift:  # an address off the 16-byte boundary takes the kernel without tensor cores
+        room = torch.empty(args[0].numel() + 1, dtype=dtype, device="cuda")
+        room[1:] = args[0].reshape(-1)
+        args[0] = room[1:].view(args[0].shape)
+    out, _, _ = c.run(args=args)
+    ro, _, _, A, S, _ = reference(c)
+    ew = (D + 1) * EPS * S + 4 * EPS * (S + 1)
+    half = torch.exp2(torch.floor(torch.log2(ro.abs().clamp(min=2.0 ** (-14 if dtype == F16 else -126))))) * (
+        torch.finfo(dtype).eps / 2)
+    tol = half + (2 * ew + (0.0 if dtype == F32 else 2.0 ** -16) + 4 * EPS)[..., None] * A
+    err = (out.double() - ro).abs()
+    assert torch.all(err <= tol), f"{float((err / tol).max())} of its bound"
