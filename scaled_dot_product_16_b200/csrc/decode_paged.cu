@@ -17,7 +17,6 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "paged.cuh"
@@ -913,17 +912,6 @@ __global__ void __launch_bounds__(kThreads) decode_f32_kernel(DecodeArgs a, floa
     __syncthreads();
   } while (c.next_unit(a));
   cp_wait<0>();
-}
-
-// Raises a kernel's limit of dynamic shared memory, once per device.
-cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& ready) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && (ready.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
-  return e;
 }
 
 template <typename T, int D, int NB>

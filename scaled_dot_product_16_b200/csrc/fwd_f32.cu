@@ -383,12 +383,16 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kerne
   }
 }
 
+// Shared memory of a block, for head sizes rounded up to multiples of 4.
+constexpr int smem_bytes(int D4, int Dv4) {
+  return (int)sizeof(float) * (kBM * D4 + kBM * kBN + 2 * kBN * ((D4 / 4 | 1) * 4) + 2 * kBN * Dv4);
+}
+
 template <int DMAX>
 cudaError_t launch_dmax(const FwdArgs& a, cudaStream_t st) {
-  const int D4 = (a.D + 3) / 4 * 4, Dv4 = (a.Dv + 3) / 4 * 4;
-  const size_t smem = sizeof(float) * (size_t)(kBM * D4 + kBM * kBN + 2 * kBN * ((D4 / 4 | 1) * 4) + 2 * kBN * Dv4);
-  cudaError_t e = cudaFuncSetAttribute(fwd_f32_kernel<DMAX>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const int smem = smem_bytes((a.D + 3) / 4 * 4, (a.Dv + 3) / 4 * 4);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fwd_f32_kernel<DMAX>), smem_bytes(DMAX, DMAX), ready);
   if (e != cudaSuccess) return e;
   int tiles_per_seq = 0;
   int64_t gx;

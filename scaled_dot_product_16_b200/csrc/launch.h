@@ -2,9 +2,24 @@
 #pragma once
 
 #include <cuda_runtime.h>
+
+#include <atomic>
 #include <stdint.h>
 
 namespace sdpa {
+
+// Raises a kernel's limit of dynamic shared memory, once per device (`ready`: a bit for each), to the most that
+// any call of it needs. The limit belongs to the kernel and not to a launch: set to what each call needs, it could
+// be lowered by another host thread between this one's setting it and its launch, which then fails.
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (ready.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+  return e;
+}
 
 // Internal mask mode of attn_fwd_sinks, beside the attn_mask values: row i at position
 // p = i + sk - sq sees key j iff j <= p and (j >= p - pre or j < sinks).
