@@ -604,7 +604,8 @@ cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t st) {
   cols = cols < 1 ? 1 : (cols > 32 ? 32 : cols);
   const int smem = (int)sizeof(int32_t) * (a.rows_in + a.rows_in * cols);
   if (smem > 48 * 1024) {  // a column of more than 6,144 rows
-    const cudaError_t e = cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fork_kernel), 2 * kMaxTableRows * (int)sizeof(int32_t), ready);
     if (e != cudaSuccess) return e;
   }
   fork_kernel<<<(a.max_pages + cols - 1) / cols, kForkThreads, smem, st>>>(a, cols);

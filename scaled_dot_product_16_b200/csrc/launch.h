@@ -142,6 +142,8 @@ struct AppendArgs {
   int num_sms;
 };
 
+constexpr int kMaxTableRows = 8192;  // rows of a page table in the calls that change it
+
 struct ForkArgs {
   const int32_t* table;
   const int32_t* src;

@@ -57,3 +57,29 @@ def test_float32_forwards_of_several_head_sizes():
     _together(jobs)
     for out, v, _ in checks:
         assert torch.equal(out, v)  # one key: its value
+
+
+def test_forks_of_tables_of_many_rows():
+    """Tables of more than 6,144 rows need more shared memory than a kernel has by default, each its own amount."""
+    lib = sdpa.load_library()
+    jobs, checks = [], []
+    for rows in (8192, 6200, 8192, 6200, 7000, 6150):
+        table = torch.arange(rows, dtype=torch.int32, device="cuda")
+        src, ref = table.flip(0).contiguous(), torch.ones(rows, dtype=torch.int32, device="cuda")
+        out, refs = torch.empty_like(table), torch.empty_like(ref)
+        stream = torch.cuda.Stream()
+        args = (table.data_ptr(), src.data_ptr(), ref.data_ptr(), None, rows, rows, 1, rows, out.data_ptr(),
+                refs.data_ptr(), None, stream.cuda_stream)
+        torch.cuda.synchronize()
+
+        def job(args=args, f=lib.attn_cache_fork):
+            for _ in range(10000):
+                rc = f(*args)
+                if rc:
+                    raise sdpa.AttnError(rc, f"attn_cache_fork of {args[4]} rows")
+
+        jobs.append(job)
+        checks.append((out, src, refs, ref, table))
+    _together(jobs)
+    for out, src, refs, ref, _ in checks:
+        assert torch.equal(out, src) and torch.equal(refs, ref)
