@@ -975,11 +975,12 @@ int64_t decode_workspace_bytes(int rows, int D) {
 
 cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t st) {
   DecodeArgs a = args;
+  const int es = a.dtype == ATTN_F32 ? 4 : 2;
   const uintptr_t all = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) |
-                        reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.p.page_stride * 2);
+                        reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.p.page_stride * es);
   if (tensor_shape(a.dtype, a.D) && (all & 15u) == 0)
     return a.dtype == ATTN_F16 ? launch_tc_t<__half>(a, st) : launch_tc_t<__nv_bfloat16>(a, st);
-  if (a.dtype == ATTN_F32 && a.D <= 128 && (all & 15u) == 0 && a.D % 4 == 0 && a.p.page_stride % 4 == 0) {
+  if (a.dtype == ATTN_F32 && a.D <= 128 && (all & 15u) == 0 && a.D % 4 == 0) {
     if (a.D <= 64) return a.rows == 4 ? launch_f32<64, 4>(a, st) : launch_f32<64, 8>(a, st);
     return a.rows == 4 ? launch_f32<128, 4>(a, st) : launch_f32<128, 8>(a, st);
   }
