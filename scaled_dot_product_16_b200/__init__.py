@@ -380,8 +380,8 @@ def _here() -> int:
 
 def _arg(x, name: str, numel: int, dt, dev: int) -> Optional[int]:
     """_ptr for a tensor that is expected to be in order: on device `dev`, dense, of torch dtype `dt`,
-    with `numel` elements or more."""
-    if (type(x) is _DEV["tensor"] and x.dtype is dt and x.get_device() == dev and x.is_contiguous()
+    with `numel` elements or more. (A tensor on the CPU is on device -1 too.)"""
+    if (type(x) is _DEV["tensor"] and x.dtype is dt and x.get_device() == dev >= 0 and x.is_contiguous()
             and x.numel() >= numel):
         return x.data_ptr()
     return _ptr(x, name, max(numel, 0), str(dt).replace("torch.", "") if dt is not None else None)

@@ -1,0 +1,37 @@
+"""Refusals of the serving calls, answered on the host without a GPU: tensors of the CPU, and sizes past the limits
+that the header states."""
+import pytest
+import torch
+
+import scaled_dot_product_16_b200 as sdpa
+from scaled_dot_product_16_b200 import build as sdpa_build
+
+BF, I32 = torch.bfloat16, torch.int32
+
+
+@pytest.fixture(scope="module")
+def lib():
+    sdpa_build.build()
+    return sdpa.load_library()
+
+
+def test_tensors_of_the_cpu_are_refused(lib):
+    """Whether a device is there or not: the first tensor that is not on it is named."""
+    B, Nq, Nkv, D, ps, mp, n = 2, 4, 2, 64, 16, 3, 5
+    x, i = torch.zeros(n * ps * Nkv * D, dtype=BF), torch.zeros(64, dtype=I32)
+    ws = torch.zeros(sdpa.attn_decode_workspace_size(Nq=Nq, Nkv=Nkv, D=D, dtype=sdpa.ATTN_BF16), dtype=torch.uint8)
+    page = dict(Nkv=Nkv, D=D, num_pages=n, page_size=ps, max_pages=mp, dtype=sdpa.ATTN_BF16, layout=sdpa.ATTN_TND)
+    calls = [
+        lambda: sdpa.attn_fwd_sinks(x, x, x, B=1, Sq=8, Skv=8, Nq=Nq, Nkv=Nkv, D=D, scale=0.1, window_tokens=4,
+                                    dtype=sdpa.ATTN_BF16, layout=sdpa.ATTN_BHSD, out=x),
+        lambda: sdpa.attn_decode_paged(x, x, x, i, i, B=B, Nq=Nq, scale=0.1, workspace=ws, out=x, **page),
+        lambda: sdpa.attn_cache_append(x, x, i, i, x, x, T=B, B=B, **page),
+        lambda: sdpa.attn_cache_fork(i, i, i, i, i, rows_in=B, rows_out=B, max_pages=mp, num_pages=n),
+        lambda: sdpa.attn_cache_reserve(i, i, i, None, i, B=B, max_pages=mp, num_pages=n, page_size=ps),
+        lambda: sdpa.attn_cache_evict(i, i, i, B=B, max_pages=mp, num_pages=n, page_size=ps, window_tokens=4),
+        lambda: sdpa.attn_cache_compact(i, i, i, i, i, i, i, rows=B, max_pages=mp, num_pages=n),
+        lambda: sdpa.attn_cache_copy(x, x, i, n_copies=2, num_pages=n, page_elems=ps * Nkv * D, dtype=sdpa.ATTN_BF16),
+    ]
+    for call in calls:
+        with pytest.raises(ValueError, match="must be on a CUDA device"):
+            call()
