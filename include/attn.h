@@ -366,7 +366,8 @@ ATTN_API int attn_fwd_sinks(const void* q, const void* k, const void* v,
  *                   the caller counts beside them); 0 = free; at most 2^16.
  * All of these are device arrays. Their contents are checked on the device: what is out of range sets
  * ATTN_ERR_DATA in the status word and is skipped as stated for each call; it is never dereferenced.
- * Tables have at most 8192 rows and 2^29 entries in the calls that change them.
+ * Tables have at most 8192 rows and 2^29 entries, and pools 2^30 pages, in the calls that change tables
+ * (ATTN_ERR_UNSUPPORTED beyond).
  */
 
 /*

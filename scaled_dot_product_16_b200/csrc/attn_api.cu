@@ -440,6 +440,7 @@ int page_args(const int32_t* page_table, const int32_t* seq_lens, int B, int Nkv
 int table_args(int rows, int max_pages, int num_pages) {
   if (rows < 0 || max_pages < 0 || num_pages < 0) return ATTN_ERR_INVALID;
   if (rows > sdpa::kMaxTableRows || (int64_t)rows * max_pages > (int64_t(1) << 29)) return ATTN_ERR_UNSUPPORTED;
+  if (num_pages > 1 << 30) return ATTN_ERR_UNSUPPORTED;  // the kernels' walks over the pool count in 32 bits
   return ATTN_OK;
 }
 

@@ -35,3 +35,15 @@ def test_tensors_of_the_cpu_are_refused(lib):
     for call in calls:
         with pytest.raises(ValueError, match="must be on a CUDA device"):
             call()
+
+
+UNSUP, MAX32 = sdpa.ATTN_ERR_UNSUPPORTED, 2 ** 31 - 1
+
+
+def test_pools_of_more_than_2_30_pages(lib):
+    """The page kernels step over the pool in 32-bit integers, 8,192 pages at a time."""
+    for n in ((1 << 30) + 1, MAX32 - 8192, MAX32):
+        assert lib.attn_cache_fork(16, 16, 16, None, 2, 2, 4, n, 32, 32, None, None) == UNSUP
+        assert lib.attn_cache_reserve(16, 16, 16, None, 2, 4, n, 16, 16, None) == UNSUP
+        assert lib.attn_cache_evict(16, 16, 16, 2, 4, n, 16, 8, 0, None) == UNSUP
+        assert lib.attn_cache_compact(16, 16, 2, 4, n, 16, 16, 16, 16, 16, None) == UNSUP
