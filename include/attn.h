@@ -360,7 +360,8 @@ ATTN_API int attn_fwd_sinks(const void* q, const void* k, const void* v,
  *                   Nkv * D apart; the two may be halves of one tensor [num_pages, 2, ...]).
  * page_table        int32 [B, max_pages]: entry [b, i] is the page of positions i * page_size ..
  *                   (i + 1) * page_size - 1 of row (sequence) b, or -1 where it has none. Pages may be
- *                   shared between rows. Every max_pages * page_size <= 2^30.
+ *                   shared between rows. Every max_pages * page_size <= 2^30, and B <= 2^30
+ *                   (ATTN_ERR_UNSUPPORTED beyond).
  * seq_lens          int32 [B]: tokens of each row, 0 <= seq_lens[b] <= max_pages * page_size.
  * ref_count         int32 [num_pages]: in how many places a page is held (table entries, and whatever
  *                   the caller counts beside them); 0 = free; at most 2^16.

@@ -421,6 +421,7 @@ int page_args(const int32_t* page_table, const int32_t* seq_lens, int B, int Nkv
   if (page_stride != 0 && page_stride < dense) return ATTN_ERR_INVALID;
   if (B > 0 && (seq_lens == nullptr || (page_table == nullptr && max_pages > 0))) return ATTN_ERR_INVALID;
   if ((int64_t)max_pages * page_size > (int64_t(1) << 30)) return ATTN_ERR_UNSUPPORTED;  // positions
+  if (B > 1 << 30) return ATTN_ERR_UNSUPPORTED;  // rows are divided and searched in 32-bit integers
   p->page_table = page_table;
   p->seq_lens = seq_lens;
   p->B = B;

@@ -47,3 +47,12 @@ def test_pools_of_more_than_2_30_pages(lib):
         assert lib.attn_cache_reserve(16, 16, 16, None, 2, 4, n, 16, 16, None) == UNSUP
         assert lib.attn_cache_evict(16, 16, 16, 2, 4, n, 16, 8, 0, None) == UNSUP
         assert lib.attn_cache_compact(16, 16, 2, 4, n, 16, 16, 16, 16, 16, None) == UNSUP
+
+
+def test_more_than_2_30_rows(lib):
+    """decode divides the rows among its threads and append searches them, in 32-bit integers."""
+    n = 1 << 40
+    for B in ((1 << 30) + 1, MAX32):
+        assert lib.attn_decode_paged(16, 16, 16, 16, 16, B, 1, 1, 64, 9, 16, 4, 0, 0.1, 8, 0, 0, 1, 16, n, 16, None,
+                                     None, None) == UNSUP
+        assert lib.attn_cache_append(16, 16, 16, 16, 16, 8, B, 8, 128, 9, 16, 4, 0, 0, 1, 16, 16, None) == UNSUP
