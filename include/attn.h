@@ -403,7 +403,7 @@ ATTN_API int attn_decode_paged(const void* q, const void* k_cache, const void* v
 /*
  * attn_cache_append -- write the keys and values of new tokens into the cache.
  *
- *   k, v        [T, Nkv, D] of `dtype`, packed row after row
+ *   k, v        [T, Nkv, D] of `dtype`, packed row after row; T <= 2^30 (ATTN_ERR_UNSUPPORTED beyond)
  *   cu_seqlens  int32 [B], cumulative tokens of each row without a leading zero, ending at T; NULL:
  *               one token per row (T = B)
  *   seq_lens    the rows' lengths WITH the new tokens: the n tokens of row b go to positions

@@ -509,6 +509,7 @@ int attn_cache_append(const void* k, const void* v, const int32_t* page_table, c
   int rc = page_args(page_table, seq_lens, B, Nkv, D, num_pages, page_size, max_pages, page_stride, layout, &a.p);
   if (rc != ATTN_OK) return rc;
   if (T < 0 || (cu_seqlens == nullptr && T != B)) return ATTN_ERR_INVALID;
+  if (T > 1 << 30) return ATTN_ERR_UNSUPPORTED;  // the kernel steps over the tokens in 32-bit integers
   if (T == 0) return ATTN_OK;
   if (B == 0) return ATTN_ERR_INVALID;
   if (k == nullptr || v == nullptr || k_cache == nullptr || v_cache == nullptr) return ATTN_ERR_INVALID;

@@ -56,3 +56,8 @@ def test_more_than_2_30_rows(lib):
         assert lib.attn_decode_paged(16, 16, 16, 16, 16, B, 1, 1, 64, 9, 16, 4, 0, 0.1, 8, 0, 0, 1, 16, n, 16, None,
                                      None, None) == UNSUP
         assert lib.attn_cache_append(16, 16, 16, 16, 16, 8, B, 8, 128, 9, 16, 4, 0, 0, 1, 16, 16, None) == UNSUP
+
+
+def test_more_than_2_30_new_tokens(lib):
+    for T in ((1 << 30) + 1, MAX32):
+        assert lib.attn_cache_append(16, 16, 16, 16, 16, T, 8, 8, 128, 9, 16, 4, 0, 0, 1, 16, 16, None) == UNSUP
