@@ -339,7 +339,8 @@ ATTN_API int attn_merge(const void* prev_out, const float* prev_max, const float
  * window_tokens >= 1 (ATTN_WINDOW_ALL or more: every key up to p, as ATTN_MASK_CAUSAL_BOTTOMRIGHT);
  * sink_tokens >= 0. Key tiles between the sinks and a block's windows are neither read nor
  * multiplied, so the cost grows with window_tokens + sink_tokens and not with Skv.
- * Other arguments, layouts, statistics, limits and errors are those of attn_fwd.
+ * Other arguments, layouts, statistics, limits and errors are those of attn_fwd; Sq, Skv <= 2^30
+ * (ATTN_ERR_UNSUPPORTED beyond).
  * NaN or infinite values in keys that a row does not see do not reach the row. In values of its own
  * sequence that it does not see they may (0 * NaN), where a key tile (128 keys; 32 for ATTN_F32) holds
  * them beside keys that rows of its block see; those of other sequences never do.

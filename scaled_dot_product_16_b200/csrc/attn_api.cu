@@ -221,6 +221,8 @@ int attn_fwd_sinks(const void* q, const void* k, const void* v, const int32_t* c
                    float scale, int64_t window_tokens, int64_t sink_tokens, int dtype, int layout,
                    void* out, float* softmax_max, float* softmax_sum, void* stream) {
   if (window_tokens < 1 || sink_tokens < 0) return ATTN_ERR_INVALID;
+  // positions are 32-bit sums of a row and the two lengths, and a window of 2^30 is one of every key
+  if (Sq > 1 << 30 || Skv > 1 << 30) return ATTN_ERR_UNSUPPORTED;
   Extras x;
   x.window = true;
   x.pre = window_tokens - 1;

@@ -61,3 +61,10 @@ def test_more_than_2_30_rows(lib):
 def test_more_than_2_30_new_tokens(lib):
     for T in ((1 << 30) + 1, MAX32):
         assert lib.attn_cache_append(16, 16, 16, 16, 16, T, 8, 8, 128, 9, 16, 4, 0, 0, 1, 16, 16, None) == UNSUP
+
+
+def test_a_window_over_more_than_2_30_keys(lib):
+    """ATTN_WINDOW_ALL is 2^30: it would not be every key there."""
+    for sq, sk in ((1, (1 << 30) + 1), (1, MAX32), ((1 << 30) + 1, 8), (MAX32, MAX32)):
+        assert lib.attn_fwd_sinks(16, 16, 16, None, None, 1, sq, sk, 1, 1, 1, 0.5, sdpa.ATTN_WINDOW_ALL, 0, 1, 0, 16,
+                                  None, None, None) == UNSUP
