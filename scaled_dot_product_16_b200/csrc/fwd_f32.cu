@@ -46,16 +46,26 @@ __device__ __forceinline__ void stage(float* dst, const float* src, bool ok) {
 }
 
 // kBN rows of D columns into rows of `ld` floats whose columns up to a multiple of 4 become zeros; rows
-// from `rows` on become zeros.
+// from `rows` on become zeros. A warp copies kBN / kWarps rows in a row, all at once where they have no more columns
+// than it has lanes (64 keys, 256 heads of 1: 22.6 us a row at a time, 20.5 so).
 __device__ __forceinline__ void stage_tile(float* dst, int ld, const float* src, int64_t stride, int rows, int D) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int D4 = (D + 3) / 4 * 4;
-  for (int r = warp; r < kBN; r += kWarps)
-    for (int c = lane; c < D4; c += 32) {
-      const bool ok = r < rows && c < D;
-      stage(dst + r * ld + c, ok ? src + r * stride + c : src, ok);
-    }
+  constexpr int kRows = kBN / kWarps;
+  const int r0 = (threadIdx.x >> 5) * kRows, lane = threadIdx.x & 31;
+  auto one = [&](int r, int c) {
+    const bool ok = r < rows && c < D;
+    stage(dst + r * ld + c, ok ? src + r * stride + c : src, ok);
+  };
+  if (D <= 8) {
+    const int l = D <= 4 ? 2 : 3, r = lane >> l;
+    if (r < kRows) one(r0 + r, lane & ((1 << l) - 1));
+  } else {
+    const int D4 = (D + 3) / 4 * 4;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      for (int c = lane; c < D4; c += 32) one(r0 + r, c);
+  }
 }
+static_assert(kBN / kWarps * 8 <= 32, "rows of up to 8 columns at once");
 
 __device__ __forceinline__ bool wait_tile(uint32_t bar, uint32_t parity) {
   if (mbar_try_wait_sleep(bar, parity, 20000)) return true;
@@ -67,8 +77,10 @@ __device__ __forceinline__ bool wait_tile(uint32_t bar, uint32_t parity) {
 
 // Three blocks an SM at head sizes up to 64, whose tiles leave the shared memory for it (4 x 16 x 1,024, window
 // 512: 487 -> 453 us; with four registers spill: 502).
-template <int DMAX>
-__global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kernel(FwdArgs a, int tiles_per_seq, int vec) {
+// VEC: rows of q, k and v are whole 16-byte chunks. The others have a kernel of their own, as both kinds of copies in
+// one take registers that the loop needs (2 x 8 x 1,128, head size 4: 200 us, apart 180).
+template <int DMAX, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32, DMAX <= 64 ? 3 : 2) fwd_f32_kernel(FwdArgs a, int tiles_per_seq) {
   extern __shared__ __align__(16) float smem[];
   const int D = a.D, Dv = a.Dv;
   const int D4 = (D + 3) / 4 * 4, Dv4 = (Dv + 3) / 4 * 4;
@@ -162,18 +174,14 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kerne
 
   const int row0 = qt * kBM;
   const int nrows = min(kBM, sq - row0);
-  // stage Q (rows past the sequence end are zero-filled)
-  if (!vec)
-    for (int r = warp; r < kBM; r += kWarps)
-      for (int d = lane; d < D4; d += 32) sQ[r * D4 + d] = r < nrows && d < D ? Q[qoff(row0 + r) + d] : 0.f;
-  constexpr int kLaneRows = kBN / kWarps;  // vec: the first lanes of each warp copy a row each
+  constexpr int kLaneRows = kBN / kWarps;  // VEC: the first lanes of each warp copy a row each
   static_assert(kBN == kBM, "rows of a tile");
   const int64_t k_stride = a.layout == ATTN_BHSD ? D : (int64_t)a.Nkv * D;
   const int64_t v_stride = a.layout == ATTN_BHSD ? Dv : (int64_t)a.Nkv * Dv;
   auto fetch = [&](int j0, int buf, int bytes) {  // the key tile at j0; `bytes` more come to its barrier
     float* kt = sK + buf * kBN * ldk;
     float* vt = sV + buf * kBN * Dv4;
-    if (!vec) {
+    if constexpr (!VEC) {
       stage_tile(kt, ldk, K + kvoff(j0), k_stride, sk - j0, D);
       stage_tile(vt, Dv4, V + voff(j0), v_stride, sk - j0, Dv);
     } else {
@@ -220,7 +228,7 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kerne
   int buf = 0, it = 0;
   const int j_first = sink_end > 0 ? 0 : kv_begin;
   if (j_first < kv_end) {
-    if (vec && lane < kLaneRows) {  // Q with the first tile
+    if (VEC && lane < kLaneRows) {  // Q with the first tile
       const int r = warp * kLaneRows + lane;
       if (r < nrows)
         bulk_load(smem_u32(sQ + r * D4), Q + qoff(row0 + r), D * 4, smem_u32(&s_full[0]));
@@ -228,12 +236,14 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX == 64 ? 3 : 2) fwd_f32_kerne
         for (int c = 0; c < D; c += 4) *reinterpret_cast<float4*>(sQ + r * D4 + c) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __syncwarp();
+    // rows past the sequence's end become zeros
+    if constexpr (!VEC) stage_tile(sQ, D4, Q + qoff(row0), a.layout == ATTN_BHSD ? D : (int64_t)a.Nq * D, nrows, D);
     fetch(j_first, 0, nrows * D * 4);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
   for (int j0 = j_first; j0 < kv_end; j0 = after(j0), buf ^= 1, ++it) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    const bool come = !vec || wait_tile(smem_u32(&s_full[buf]), (it >> 1) & 1);
+    const bool come = !VEC || wait_tile(smem_u32(&s_full[buf]), (it >> 1) & 1);
     // this tile is there (and Q, on the first pass), and the last one is consumed
     if (__syncthreads_or(!come)) {
       if (threadIdx.x == 0) report(a.status, ATTN_ERR_TIMEOUT);
@@ -388,11 +398,11 @@ constexpr int smem_bytes(int D4, int Dv4) {
   return (int)sizeof(float) * (kBM * D4 + kBM * kBN + 2 * kBN * ((D4 / 4 | 1) * 4) + 2 * kBN * Dv4);
 }
 
-template <int DMAX>
-cudaError_t launch_dmax(const FwdArgs& a, cudaStream_t st) {
+template <int DMAX, bool VEC>
+cudaError_t launch_kernel(const FwdArgs& a, cudaStream_t st) {
   const int smem = smem_bytes((a.D + 3) / 4 * 4, (a.Dv + 3) / 4 * 4);
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fwd_f32_kernel<DMAX>), smem_bytes(DMAX, DMAX), ready);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fwd_f32_kernel<DMAX, VEC>), smem_bytes(DMAX, DMAX), ready);
   if (e != cudaSuccess) return e;
   int tiles_per_seq = 0;
   int64_t gx;
@@ -405,15 +415,21 @@ cudaError_t launch_dmax(const FwdArgs& a, cudaStream_t st) {
   if (gx <= 0) return cudaSuccess;
   if (gx * a.Nq > 0x7fffffff) return cudaErrorInvalidConfiguration;  // 2^36 query rows and more
   const unsigned grid = (unsigned)(gx * a.Nq);
-  const uintptr_t all = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
-  const int vec = (all & 15u) == 0 && a.D % 4 == 0 && a.Dv % 4 == 0;
-  fwd_f32_kernel<DMAX><<<grid, kWarps * 32, smem, st>>>(a, tiles_per_seq, vec);
+  fwd_f32_kernel<DMAX, VEC><<<grid, kWarps * 32, smem, st>>>(a, tiles_per_seq);
   return cudaGetLastError();
+}
+
+template <int DMAX>
+cudaError_t launch_dmax(const FwdArgs& a, cudaStream_t st) {
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
+  const bool vec = (all & 15u) == 0 && a.D % 4 == 0 && a.Dv % 4 == 0;
+  return vec ? launch_kernel<DMAX, true>(a, st) : launch_kernel<DMAX, false>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_fwd_f32(const FwdArgs& a, cudaStream_t st) {
+  if (a.D <= 32) return launch_dmax<32>(a, st);
   if (a.D <= 64) return launch_dmax<64>(a, st);
   if (a.D <= 96) return launch_dmax<96>(a, st);
   if (a.D <= 128) return launch_dmax<128>(a, st);
