@@ -47,7 +47,7 @@ __device__ __forceinline__ void stage(float* dst, const float* src, bool ok) {
 
 // kBN rows of D columns into rows of `ld` floats whose columns up to a multiple of 4 become zeros; rows
 // from `rows` on become zeros. A warp copies kBN / kWarps rows in a row, all at once where they have no more columns
-// than it has lanes (64 keys, 256 heads of 1: 22.6 us a row at a time, 20.5 so).
+// than it has lanes (2 x 8 x 1,128, head size 1: 266 us with a row at a time and the kernel of head sizes up to 64, 168 so).
 __device__ __forceinline__ void stage_tile(float* dst, int ld, const float* src, int64_t stride, int rows, int D) {
   constexpr int kRows = kBN / kWarps;
   const int r0 = (threadIdx.x >> 5) * kRows, lane = threadIdx.x & 31;
@@ -80,7 +80,7 @@ __device__ __forceinline__ bool wait_tile(uint32_t bar, uint32_t parity) {
 // VEC: rows of q, k and v are whole 16-byte chunks. The others have a kernel of their own, as both kinds of copies in
 // one take registers that the loop needs (2 x 8 x 1,128, head size 4: 200 us, apart 180).
 template <int DMAX, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32, DMAX <= 64 ? 3 : 2) fwd_f32_kernel(FwdArgs a, int tiles_per_seq) {
+__global__ void __launch_bounds__(kWarps * 32, DMAX <= 64 ? 3 : 2) fwd_f32_kernel(FwdArgs a, int tiles_per_seq, int x0) {
   extern __shared__ __align__(16) float smem[];
   const int D = a.D, Dv = a.Dv;
   const int D4 = (D + 3) / 4 * 4, Dv4 = (Dv + 3) / 4 * 4;
@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kWarps * 32, DMAX <= 64 ? 3 : 2) fwd_f32_kerne
   // Blocks start in the order of their index: the heads of a query tile side by side, and the last tiles of
   // the sequences first, as a causal mask gives those the most keys and a long block that starts late ends
   // late (2 x 8 x 1,128 x 128, causal: 390 -> 266 us).
-  const int x = blockIdx.x / a.Nq, h = blockIdx.x - x * a.Nq;
+  const int xb = blockIdx.x / a.Nq, h = blockIdx.x - xb * a.Nq;
+  const int x = x0 + xb;
   const int g = h / (a.Nq / a.Nkv);
 
   // ---- which (sequence, query tile) this block owns -------------------------------------
@@ -413,10 +414,16 @@ cudaError_t launch_kernel(const FwdArgs& a, cudaStream_t st) {
     gx = (a.Sq + kBM - 1) / kBM + a.B;  // upper bound on the tiles of a packed batch
   }
   if (gx <= 0) return cudaSuccess;
-  if (gx * a.Nq > 0x7fffffff) return cudaErrorInvalidConfiguration;  // 2^36 query rows and more
-  const unsigned grid = (unsigned)(gx * a.Nq);
-  fwd_f32_kernel<DMAX, VEC><<<grid, kWarps * 32, smem, st>>>(a, tiles_per_seq);
-  return cudaGetLastError();
+  if (gx > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  // as many query tiles a launch as a grid holds with all their heads (one launch but for 2^31 blocks and more)
+  const int64_t per = 0x7fffffff / a.Nq;
+  for (int64_t x0 = 0; x0 < gx; x0 += per) {
+    const unsigned grid = (unsigned)((gx - x0 < per ? gx - x0 : per) * a.Nq);
+    fwd_f32_kernel<DMAX, VEC><<<grid, kWarps * 32, smem, st>>>(a, tiles_per_seq, (int)x0);
+    const cudaError_t launched = cudaGetLastError();
+    if (launched != cudaSuccess) return launched;
+  }
+  return cudaSuccess;
 }
 
 template <int DMAX>
