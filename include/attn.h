@@ -13,8 +13,8 @@
  *                    caller-owned buffer that attn_sparse_csr_tc_planned then reads.
  *   attn_fwd_sinks   attn_fwd through a sliding window of the newest keys and the first few keys.
  *   attn_decode_paged  the same for one new token per sequence, over a paged key/value cache.
- *   attn_cache_append, attn_cache_fork, attn_cache_reserve, attn_cache_evict, attn_cache_compact,
- *   attn_cache_copy  that cache: new tokens written into its pages, and the bookkeeping of the pages.
+ *   attn_cache_append, attn_cache_fork, attn_cache_reserve, attn_cache_grow, attn_cache_evict,
+ *   attn_cache_compact, attn_cache_copy  that cache: new tokens written into its pages, and the bookkeeping of the pages.
  *
  * Conventions shared by every call
  *   - All tensor pointers are DEVICE pointers owned by the caller. The library allocates no
@@ -409,6 +409,7 @@ ATTN_API int attn_decode_paged(const void* q, const void* k_cache, const void* v
  *               one token per row (T = B)
  *   seq_lens    the rows' lengths WITH the new tokens: the n tokens of row b go to positions
  *               seq_lens[b] - n .. seq_lens[b] - 1
+ *               A row of length 0 has no new tokens: those that T or cu_seqlens give it are skipped.
  * The pages must be there and the row's own (attn_cache_reserve); positions of two rows that share a
  * page would be written twice. No other position is touched.
  * Data errors: cumulative lengths that decrease or do not end at T; a token whose position is outside
@@ -455,6 +456,23 @@ ATTN_API int attn_cache_fork(const int32_t* page_table, const int32_t* src_rows,
 ATTN_API int attn_cache_reserve(int32_t* page_table, int32_t* ref_count, const int32_t* seq_lens,
                                 const int32_t* new_tokens, int B, int max_pages, int num_pages,
                                 int page_size, int32_t* copies, void* stream);
+
+/*
+ * attn_cache_grow -- attn_cache_reserve that also keeps the lengths, so that a step which is refused stays one
+ * that never was, though the host does not wait to learn of it.
+ *
+ *   seq_lens    the rows' lengths WITHOUT the new tokens
+ *   new_tokens  int32 [B]; NULL: one per row, with live_only = 1 only for rows that are not empty (rows that have
+ *               ended stay so)
+ *   new_lens    int32 [B], output
+ * Where attn_cache_reserve of those lengths plus new tokens succeeds: the same, seq_lens[b] += new_tokens[b], and
+ * new_lens[b] is the new length, or 0 where row b got no tokens. Where it records an error: the same error,
+ * seq_lens too is as before, and new_lens is all 0. attn_cache_append with new_lens as its seq_lens then
+ * writes the tokens of the rows that have pages for them, and no others. No overlap among the arrays.
+ */
+ATTN_API int attn_cache_grow(int32_t* page_table, int32_t* ref_count, int32_t* seq_lens,
+                             const int32_t* new_tokens, int live_only, int B, int max_pages, int num_pages,
+                             int page_size, int32_t* copies, int32_t* new_lens, void* stream);
 
 /*
  * attn_cache_evict -- let go of pages that a window has left behind, in place.

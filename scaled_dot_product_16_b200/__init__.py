@@ -3,8 +3,8 @@
 The operations (attn_fwd, attn_fwd_masked, attn_fwd_accumulate, attn_sparse_csr,
 attn_sparse_csr_tc, attn_csr_plan_size, attn_csr_plan, attn_sparse_csr_tc_planned, attn_merge,
 attn_fwd_sinks, attn_decode_workspace_size, attn_decode_paged, attn_cache_append, attn_cache_fork,
-attn_cache_reserve, attn_cache_evict, attn_cache_compact, attn_cache_copy, attn_get_last_error) are the
-C-ABI calls declared in ``include/attn.h``; the functions here carry the same names and only marshal
+attn_cache_reserve, attn_cache_grow, attn_cache_evict, attn_cache_compact, attn_cache_copy,
+attn_get_last_error) are the C-ABI calls declared in ``include/attn.h``; the functions here carry the same names and only marshal
 arguments (tensor data pointers, sizes, the current CUDA stream) into them. Every step of the
 computation runs in the library's CUDA kernels. There is no CPU path: if ``libattn.so`` is missing the first call raises.
 
@@ -26,7 +26,7 @@ __all__ = [
     "load_library", "attn_fwd_masked", "attn_sparse_csr_tc", "attn_csr_plan_size", "attn_csr_plan",
     "attn_sparse_csr_tc_planned", "attn_sparse_csr_tc_noalloc", "attn_fwd_sinks",
     "attn_decode_workspace_size", "attn_decode_paged", "attn_cache_append", "attn_cache_fork",
-    "attn_cache_reserve", "attn_cache_evict", "attn_cache_compact", "attn_cache_copy", "ATTN_WINDOW_ALL",
+    "attn_cache_reserve", "attn_cache_grow", "attn_cache_evict", "attn_cache_compact", "attn_cache_copy", "ATTN_WINDOW_ALL",
 ]
 
 (ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_DATA, ATTN_ERR_TIMEOUT,
@@ -97,6 +97,8 @@ def load_library():
         lib.attn_cache_fork.restype = I
         lib.attn_cache_reserve.argtypes = [P, P, P, P, I, I, I, I, P, P]
         lib.attn_cache_reserve.restype = I
+        lib.attn_cache_grow.argtypes = [P, P, P, P, I, I, I, I, I, P, P, P]
+        lib.attn_cache_grow.restype = I
         lib.attn_cache_evict.argtypes = [P, P, P, I, I, I, I, I64, I64, P]
         lib.attn_cache_evict.restype = I
         lib.attn_cache_compact.argtypes = [P, P, I, I, I, P, P, P, P, P, P]
@@ -535,6 +537,23 @@ def attn_cache_reserve(page_table, ref_count, seq_lens, new_tokens, copies, *, B
         _arg(copies, "copies", 2 * B, i32, dev), _on(stream, dev))
     if rc:
         _check(rc, "attn_cache_reserve")
+
+
+def attn_cache_grow(page_table, ref_count, seq_lens, new_tokens, new_lens, copies, *, B: int, max_pages: int,
+                    num_pages: int, page_size: int, live_only: bool = False, stream=None) -> None:
+    """attn_cache_reserve that also adds the new tokens to the lengths, unless it is refused (see
+    ``attn_cache_grow`` in include/attn.h). `new_tokens` may be None (one per row, or per row that is not empty)."""
+    lib, dev = _lib or load_library(), _here()
+    i32 = _DEV["i32"]
+    rc = _call(
+        lib.attn_cache_grow,
+        _arg(page_table, "page_table", B * max_pages, i32, dev), _arg(ref_count, "ref_count", num_pages, i32, dev),
+        _arg(seq_lens, "seq_lens", B, i32, dev),
+        None if new_tokens is None else _arg(new_tokens, "new_tokens", B, i32, dev), int(live_only), B, max_pages,
+        num_pages, page_size, _arg(copies, "copies", 2 * B, i32, dev), _arg(new_lens, "new_lens", B, i32, dev),
+        _on(stream, dev))
+    if rc:
+        _check(rc, "attn_cache_grow")
 
 
 def attn_cache_evict(page_table, ref_count, seq_lens, *, B: int, max_pages: int, num_pages: int, page_size: int,

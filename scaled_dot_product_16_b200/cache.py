@@ -12,7 +12,7 @@ reserve, append and attend can be captured into a CUDA graph and replayed.
     for layer in range(32):
         cache.prefill(layer, q, k, v, cu_seqlens, out)           # attention of the prompts, into the cache
     while ...:
-        cache.reserve()                                          # one more token per row
+        cache.reserve(live_only=True)                            # one more token per row that has not ended
         for layer in range(32):
             cache.append(layer, k, v)
             cache.attend(layer, q, out)
@@ -26,7 +26,7 @@ import torch
 
 from . import (ATTN_BF16, ATTN_BHSD, ATTN_F16, ATTN_F32, ATTN_OK, ATTN_TND, ATTN_WINDOW_ALL, AttnError,
                attn_cache_append, attn_cache_compact, attn_cache_copy, attn_cache_evict, attn_cache_fork,
-               attn_cache_reserve, attn_decode_paged, attn_decode_workspace_size, attn_fwd_sinks,
+               attn_cache_grow, attn_decode_paged, attn_decode_workspace_size, attn_fwd_sinks,
                attn_get_last_error)
 
 _DTYPE = {ATTN_BF16: torch.bfloat16, ATTN_F32: torch.float32, ATTN_F16: torch.float16}
@@ -51,7 +51,7 @@ class PagedCache:
         self.page_table = torch.full((rows, max_pages), -1, **i32)
         self.ref_count = torch.zeros(num_pages, **i32)
         self.seq_lens = torch.zeros(rows, **i32)
-        self._ones = torch.ones(rows, **i32)
+        self.new_lens = torch.zeros(rows, **i32)  # lengths of the rows that the last reserve gave tokens, else 0
         self._copies = torch.empty((rows, 2), **i32)
         self._moves = torch.empty((max(1, num_pages // 2), 2), **i32)
         self.page_map = torch.empty(num_pages, **i32)
@@ -68,20 +68,22 @@ class PagedCache:
             attn_cache_copy(self.pool[layer, 0], self.pool[layer, 1], pairs, n_copies=n, num_pages=self.num_pages,
                             page_elems=self.page_size * self.Nkv * self.D, dtype=self.dtype)
 
-    def reserve(self, new_tokens=None) -> None:
-        """The rows are about to get `new_tokens` (int32 [rows] on the device; None: one each) more tokens: adds
-        them to the lengths and gives every row pages of its own for them. Where too few pages are free the
-        table stays as it was and check() raises; the lengths then count tokens that have no page."""
-        new = self._ones if new_tokens is None else new_tokens
-        self.seq_lens.add_(new)
-        attn_cache_reserve(self.page_table, self.ref_count, self.seq_lens, new, self._copies, B=self.rows,
-                           max_pages=self.max_pages, num_pages=self.num_pages, page_size=self.page_size)
+    def reserve(self, new_tokens=None, *, live_only: bool = False) -> None:
+        """The rows are about to get `new_tokens` (int32 [rows] on the device; None: one each, with `live_only` one for
+        each row that is not empty) more tokens: gives every row pages of its own for them and adds them to the
+        lengths. Where too few pages are free nothing changes and check() raises; the rest of the step then does no
+        harm (append writes nothing, attend sees the tokens from before), and once pages are free reserve can be
+        called again."""
+        attn_cache_grow(self.page_table, self.ref_count, self.seq_lens, new_tokens, self.new_lens, self._copies,
+                        B=self.rows, max_pages=self.max_pages, num_pages=self.num_pages, page_size=self.page_size,
+                        live_only=live_only)
         self._copy(self._copies, self.rows)
 
     def append(self, layer: int, k, v, cu_seqlens=None) -> None:
         """Writes the reserved tokens' keys and values [T, Nkv, D], packed row after row (cumulative tokens
-        cu_seqlens as attn_cache_append takes them; None: one per row)."""
-        attn_cache_append(k, v, self.page_table, self.seq_lens, self.pool[layer, 0], self.pool[layer, 1],
+        cu_seqlens as attn_cache_append takes them; None: one per row). Tokens of rows for which the last reserve had
+        none, or was refused, are skipped. No fork comes between the two."""
+        attn_cache_append(k, v, self.page_table, self.new_lens, self.pool[layer, 0], self.pool[layer, 1],
                           cu_seqlens=cu_seqlens, T=k.shape[0], B=self.rows, **self._sizes())
 
     def attend(self, layer: int, q, out, softmax_max=None, softmax_sum=None) -> None:

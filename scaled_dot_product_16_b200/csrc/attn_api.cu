@@ -67,7 +67,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 extern "C" {
 
-int attn_abi_version(void) { return (1 << 16) | 4; }  // 1.4: attn_fwd_sinks, the paged cache calls
+int attn_abi_version(void) { return (1 << 16) | 5; }  // 1.5: attn_cache_grow
 
 const char* attn_status_string(int s) {
   switch (s) {
@@ -449,6 +449,37 @@ int table_args(int rows, int max_pages, int num_pages) {
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
+// attn_cache_reserve, and with lens_out and new_lens attn_cache_grow
+int reserve_impl(int32_t* page_table, int32_t* ref_count, const int32_t* seq_lens, const int32_t* new_tokens, int B,
+                 int max_pages, int num_pages, int page_size, int32_t* copies, int32_t* lens_out, int32_t* new_lens,
+                 bool live_only, void* stream) {
+  int rc = table_args(B, max_pages, num_pages);
+  if (rc != ATTN_OK) return rc;
+  if (page_size < 1) return ATTN_ERR_INVALID;
+  if ((int64_t)max_pages * page_size > (int64_t(1) << 30)) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0) return ATTN_OK;
+  if (seq_lens == nullptr || copies == nullptr) return ATTN_ERR_INVALID;
+  if (max_pages > 0 && page_table == nullptr) return ATTN_ERR_INVALID;
+  if (num_pages > 0 && ref_count == nullptr) return ATTN_ERR_INVALID;
+  sdpa::ReserveArgs a{};
+  a.table = page_table;
+  a.ref = ref_count;
+  a.lens = seq_lens;
+  a.new_tokens = new_tokens;
+  a.copies = copies;
+  a.lens_out = lens_out;
+  a.new_lens = new_lens;
+  a.live_only = live_only;
+  a.B = B;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  int sms = 0;
+  rc = device_state(&a.status, &sms);
+  if (rc != ATTN_OK) return rc;
+  return from_cuda(sdpa::launch_cache_reserve(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -562,28 +593,17 @@ int attn_cache_fork(const int32_t* page_table, const int32_t* src_rows, const in
 int attn_cache_reserve(int32_t* page_table, int32_t* ref_count, const int32_t* seq_lens,
                        const int32_t* new_tokens, int B, int max_pages, int num_pages, int page_size,
                        int32_t* copies, void* stream) {
-  int rc = table_args(B, max_pages, num_pages);
-  if (rc != ATTN_OK) return rc;
-  if (page_size < 1) return ATTN_ERR_INVALID;
-  if ((int64_t)max_pages * page_size > (int64_t(1) << 30)) return ATTN_ERR_UNSUPPORTED;
-  if (B == 0) return ATTN_OK;
-  if (seq_lens == nullptr || copies == nullptr) return ATTN_ERR_INVALID;
-  if (max_pages > 0 && page_table == nullptr) return ATTN_ERR_INVALID;
-  if (num_pages > 0 && ref_count == nullptr) return ATTN_ERR_INVALID;
-  sdpa::ReserveArgs a{};
-  a.table = page_table;
-  a.ref = ref_count;
-  a.lens = seq_lens;
-  a.new_tokens = new_tokens;
-  a.copies = copies;
-  a.B = B;
-  a.max_pages = max_pages;
-  a.num_pages = num_pages;
-  a.page_size = page_size;
-  int sms = 0;
-  rc = device_state(&a.status, &sms);
-  if (rc != ATTN_OK) return rc;
-  return from_cuda(sdpa::launch_cache_reserve(a, static_cast<cudaStream_t>(stream)));
+  return reserve_impl(page_table, ref_count, seq_lens, new_tokens, B, max_pages, num_pages, page_size, copies,
+                      nullptr, nullptr, false, stream);
+}
+
+int attn_cache_grow(int32_t* page_table, int32_t* ref_count, int32_t* seq_lens, const int32_t* new_tokens,
+                    int live_only, int B, int max_pages, int num_pages, int page_size, int32_t* copies,
+                    int32_t* new_lens, void* stream) {
+  if (live_only != 0 && live_only != 1) return ATTN_ERR_INVALID;
+  if (B > 0 && (new_lens == nullptr || new_lens == seq_lens || new_lens == new_tokens)) return ATTN_ERR_INVALID;
+  return reserve_impl(page_table, ref_count, seq_lens, new_tokens, B, max_pages, num_pages, page_size, copies,
+                      seq_lens, new_lens, live_only != 0, stream);
 }
 
 int attn_cache_evict(int32_t* page_table, int32_t* ref_count, const int32_t* seq_lens, int B, int max_pages,

@@ -60,7 +60,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a,
       if (b == a.p.B) continue;  // behind the last row: reported above
       left = __ldg(a.cu + b) - t;
     }
-    const int64_t pos = (int64_t)__ldg(a.p.seq_lens + b) - left;
+    const int len = __ldg(a.p.seq_lens + b);
+    if (len == 0) continue;  // no new tokens after all (attn_cache_grow)
+    const int64_t pos = (int64_t)len - left;
     if (pos < 0 || pos >= (int64_t)a.p.max_pages * a.p.page_size) {
       if (lane == 0) report(a.status, ATTN_ERR_DATA);
       continue;
@@ -204,7 +206,8 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkArgs a, int cols
 // One block. A slot is a (row, column) whose page the row's next tokens go to: it needs a free page
 // if it has none, or if its page is shared (count > 1). Where every holder of a page asks for it in
 // the same call the first of them, in slot order, keeps it. Nothing is changed unless enough pages
-// are free.
+// are free. attn_cache_grow is the same with the lengths kept here too, so that what follows on the device (append)
+// can tell a step that was refused.
 //
 // The counts themselves carry the bookkeeping between the passes (a count is at most kMaxCount and there
 // are at most 8192 slots of one page, one per row): every asking slot takes 2^17 off its shared page's
@@ -263,15 +266,25 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
   const int tid = threadIdx.x;
   if (tid == 0) s.bad = 0;
   __syncthreads();
+  const bool grow = a.new_lens != nullptr;  // attn_cache_grow: the lengths are without the new tokens
+  auto added = [&](int b) -> int {
+    return a.new_tokens != nullptr ? a.new_tokens[b] : a.live_only ? a.lens[b] > 0 : 1;
+  };
   auto span = [&](int b, int* start, int* i0) -> int {  // slots of row b
-    const int len = a.lens[b], add = a.new_tokens != nullptr ? a.new_tokens[b] : 1;
-    if (add < 0 || len < add || (int64_t)len > (int64_t)a.max_pages * a.page_size) {
+    const int add = added(b);
+    const int64_t first = grow ? (int64_t)a.lens[b] : (int64_t)a.lens[b] - add;
+    if (add < 0 || first < 0 || first + add > (int64_t)a.max_pages * a.page_size) {
       s.bad = 1;
       return 0;
     }
-    *start = len - add;
+    *start = (int)first;
     *i0 = *start / a.page_size;
-    return add == 0 ? 0 : (len - 1) / a.page_size - *i0 + 1;
+    return add == 0 ? 0 : (*start + add - 1) / a.page_size - *i0 + 1;
+  };
+  auto refuse = [&](int status) {
+    if (tid == 0) report(a.status, status);
+    if (grow)
+      for (int b = tid; b < a.B; b += kResThreads) a.new_lens[b] = 0;
   };
   // the slots of each row, and the first slot of it
   int slots = 0;
@@ -288,7 +301,7 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
   }
   __syncthreads();
   if (s.bad) {
-    if (tid == 0) report(a.status, ATTN_ERR_DATA);
+    refuse(ATTN_ERR_DATA);
     return;
   }
   // A slot: its row and table entry, and whether an earlier token of the row lies in its page. Each
@@ -325,7 +338,7 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
   }
   __syncthreads();
   if (s.bad) {
-    if (tid == 0) report(a.status, ATTN_ERR_DATA);
+    refuse(ATTN_ERR_DATA);
     return;
   }
   // 1: every slot of a shared page asks for it
@@ -394,7 +407,7 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
       const int page = *slot_at(x).e;
       if (page >= 0 && a.ref[page] < kOwned) atomicAnd(a.ref + page, INT32_MAX);
     }
-    if (tid == 0) report(a.status, s.bad ? ATTN_ERR_DATA : ATTN_ERR_PAGES);
+    refuse(s.bad ? ATTN_ERR_DATA : ATTN_ERR_PAGES);
     return;
   }
   // 4: hand out the pages, kResThreads slots at a time
@@ -451,6 +464,13 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
   for (int x = tid; x < slots; x += kResThreads) {
     const int page = *slot_at(x).e;
     if (a.ref[page] == INT32_MIN + x) a.ref[page] = 1;
+  }
+  if (!grow) return;
+  __syncthreads();  // the old lengths have been read
+  for (int b = tid; b < a.B; b += kResThreads) {
+    const int add = added(b), len = a.lens[b] + add;
+    a.lens_out[b] = len;
+    a.new_lens[b] = add > 0 ? len : 0;
   }
 }
 

@@ -162,6 +162,9 @@ struct ReserveArgs {
   const int32_t* lens;
   const int32_t* new_tokens;  // null: one per row
   int32_t* copies;            // [B, 2]
+  int32_t* lens_out;          // attn_cache_grow: lens; null with new_lens otherwise
+  int32_t* new_lens;          // [B]
+  bool live_only;             // without new_tokens: empty rows get none
   int B, max_pages, num_pages, page_size;
   int* status;
 };

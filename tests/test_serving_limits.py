@@ -68,3 +68,20 @@ def test_a_window_over_more_than_2_30_keys(lib):
     for sq, sk in ((1, (1 << 30) + 1), (1, MAX32), ((1 << 30) + 1, 8), (MAX32, MAX32)):
         assert lib.attn_fwd_sinks(16, 16, 16, None, None, 1, sq, sk, 1, 1, 1, 0.5, sdpa.ATTN_WINDOW_ALL, 0, 1, 0, 16,
                                   None, None, None) == UNSUP
+
+
+def test_grow_refuses_what_reserve_does(lib):
+    INVALID, OK = sdpa.ATTN_ERR_INVALID, sdpa.ATTN_OK
+    d = dict(table=16, ref=16, lens=16, new=None, live=0, B=2, max_pages=4, num_pages=9, page_size=16, copies=16,
+             new_lens=32, stream=None)
+
+    def f(**kw):
+        return lib.attn_cache_grow(*dict(d, **kw).values())
+
+    for bad in (dict(B=-1), dict(page_size=0), dict(lens=None), dict(copies=None), dict(table=None), dict(ref=None),
+                dict(new_lens=None), dict(new_lens=16), dict(new=32), dict(live=2), dict(live=-1)):
+        assert f(**bad) == INVALID, bad
+    assert f(B=8193) == UNSUP and f(page_size=1 << 29) == UNSUP and f(num_pages=MAX32) == UNSUP and f(B=0) == OK
+    i = torch.zeros(64, dtype=I32)
+    with pytest.raises(ValueError, match="must be on a CUDA device"):
+        sdpa.attn_cache_grow(i, i, i, None, i, i, B=2, max_pages=3, num_pages=5, page_size=4)
