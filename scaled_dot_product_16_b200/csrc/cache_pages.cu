@@ -425,9 +425,11 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
     }
     const int rank = given + block_scan(need, s.warp, &sum);
     if (given + sum > listed + kResThreads) {
-      // list free pages given .. given + kResThreads - 1: those handed out so far are no longer free
+      // list free pages given .. given + kResThreads - 1, or as many as are still needed, and not only this step's: the
+      // next steps take theirs from here too. Those handed out so far are no longer free.
       int found = given;
-      for (int p0 = 0; p0 < a.num_pages && found < given + sum; p0 += kResThreads * kScan) {
+      const int upto = min(given + kResThreads, needed);
+      for (int p0 = 0; p0 < a.num_pages && found < upto; p0 += kResThreads * kScan) {
         int r[kScan], n = 0, more;
         load_counts(a.ref, p0 + tid * kScan, a.num_pages, 1, r);
 #pragma unroll
