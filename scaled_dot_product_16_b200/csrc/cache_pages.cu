@@ -260,19 +260,20 @@ __device__ __forceinline__ void load_counts(const int32_t* ref, int p, int n, in
   }
 }
 
-__global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
+// GROW: attn_cache_grow, whose lengths come without the new tokens.
+template <bool GROW>
+__global__ void __launch_bounds__(kResThreads, 1) reserve_kernel(ReserveArgs a) {
   __shared__ ResSmem s;
   extern __shared__ int32_t prefix[];  // [B] first slot of each row
   const int tid = threadIdx.x;
   if (tid == 0) s.bad = 0;
   __syncthreads();
-  const bool grow = a.new_lens != nullptr;  // attn_cache_grow: the lengths are without the new tokens
   auto added = [&](int b) -> int {
-    return a.new_tokens != nullptr ? a.new_tokens[b] : a.live_only ? a.lens[b] > 0 : 1;
+    return a.new_tokens != nullptr ? a.new_tokens[b] : GROW && a.live_only ? a.lens[b] > 0 : 1;
   };
   auto span = [&](int b, int* start, int* i0) -> int {  // slots of row b
     const int add = added(b);
-    const int64_t first = grow ? (int64_t)a.lens[b] : (int64_t)a.lens[b] - add;
+    const int64_t first = GROW ? (int64_t)a.lens[b] : (int64_t)a.lens[b] - add;
     if (add < 0 || first < 0 || first + add > (int64_t)a.max_pages * a.page_size) {
       s.bad = 1;
       return 0;
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
   };
   auto refuse = [&](int status) {
     if (tid == 0) report(a.status, status);
-    if (grow)
+    if constexpr (GROW)
       for (int b = tid; b < a.B; b += kResThreads) a.new_lens[b] = 0;
   };
   // the slots of each row, and the first slot of it
@@ -467,12 +468,13 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(ReserveArgs a) {
     const int page = *slot_at(x).e;
     if (a.ref[page] == INT32_MIN + x) a.ref[page] = 1;
   }
-  if (!grow) return;
-  __syncthreads();  // the old lengths have been read
-  for (int b = tid; b < a.B; b += kResThreads) {
-    const int add = added(b), len = a.lens[b] + add;
-    a.lens_out[b] = len;
-    a.new_lens[b] = add > 0 ? len : 0;
+  if constexpr (GROW) {
+    __syncthreads();  // the old lengths have been read
+    for (int b = tid; b < a.B; b += kResThreads) {
+      const int add = added(b), len = a.lens[b] + add;
+      a.lens_out[b] = len;
+      a.new_lens[b] = add > 0 ? len : 0;
+    }
   }
 }
 
@@ -635,7 +637,11 @@ cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_cache_reserve(const ReserveArgs& a, cudaStream_t st) {
-  reserve_kernel<<<1, kResThreads, sizeof(int32_t) * a.B, st>>>(a);
+  const size_t smem = sizeof(int32_t) * a.B;
+  if (a.new_lens != nullptr)
+    reserve_kernel<true><<<1, kResThreads, smem, st>>>(a);
+  else
+    reserve_kernel<false><<<1, kResThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
