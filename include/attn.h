@@ -450,8 +450,9 @@ ATTN_API int attn_cache_fork(const int32_t* page_table, const int32_t* src_rows,
  * earlier tokens of its row has to be copied: copies int32 [B, 2] gets (source, destination) for each
  * row, or (-1, -1), for attn_cache_copy (once per layer whose caches share the table).
  * All or nothing: where fewer pages are free than needed, ATTN_ERR_PAGES is recorded; where a length,
- * an entry or a count is out of range (a held page with count 0, or with fewer than ask for it), ATTN_ERR_DATA. page_table
- * and ref_count are then as before, and copies is all -1.
+ * an entry or a count is out of range (a held page with count 0, or with fewer than ask for it), or where more than
+ * 8192 of the entries for the new tokens hold one shared page, ATTN_ERR_DATA. page_table and ref_count are then as
+ * before, and copies is all -1.
  */
 ATTN_API int attn_cache_reserve(int32_t* page_table, int32_t* ref_count, const int32_t* seq_lens,
                                 const int32_t* new_tokens, int B, int max_pages, int num_pages,
