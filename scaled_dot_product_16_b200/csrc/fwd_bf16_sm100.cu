@@ -400,6 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // are short of issue slots, not of the MUFU unit: 74 -> 70 us for 16 heads of 64), with sinks fewer, as the
   // polynomial is longer (one pair in 8 instead of 5: 181 -> 180 us for the packed case).
   constexpr int kEmu = kOwnP ? 0 : EXT == 3 ? 8 : kEmuEvery;
+  // attn_fwd_sinks, fp16: P is kept times up to 2^7, relative to m = max - 7, as fp16 has fewer bits below 2^-14 and
+  // none below 2^-25: many small weights behind one large one (a sink) count. With the 2^8 that the maximum may lag
+  // behind, P stays within 2^15. Scores of 2^20 and more, whose own rounding is no longer small, go without.
+  constexpr float kLift = EXT == 3 && F16 ? 7.f : 0.f;
+  auto lift = [](float tmax2) -> float { return kLift > 0.f && fabsf(tmax2) < 1048576.f ? kLift : 0.f; };
   constexpr int kScrubbers = EXT == 3 ? 1 : 0;
   constexpr int kIssuers = kOwnP ? 2 : 1;  // warps that issue MMAs (they and the softmax warps read each item)
   extern __shared__ uint8_t smem_raw[];
@@ -811,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmax = fmaxf(tmax, s[c]);
           }
           mraw = tmax;
-          m = tmax * scale_log2;
+          m = tmax * scale_log2 - lift(tmax * scale_log2);
           const float muse = m == -INFINITY ? 0.f : m;
           uint32_t pk[32];
 #pragma unroll
@@ -939,11 +944,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    fmaxf(mx[6], mx[7]));
           mraw = fmaxf(mraw, tmax);
           const float tmax2 = tmax * scale_log2;
-          bool bump = tmax2 > m + kRescaleThreshold;  // also true for the first finite max
+          const float up = lift(tmax2);
+          bool bump = tmax2 > m + (kRescaleThreshold + up);  // also true for the first finite max
           float corr = 1.f;
           if (bump) {
-            corr = (m == -INFINITY) ? 0.f : ex2(m - tmax2);
-            m = tmax2;
+            const float ref = tmax2 - up;
+            corr = (m == -INFINITY) ? 0.f : ex2(m - ref);
+            m = ref;
             l *= corr;
           }
           const float muse = m == -INFINITY ? 0.f : m;
