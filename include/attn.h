@@ -341,8 +341,9 @@ ATTN_API int attn_merge(const void* prev_out, const float* prev_max, const float
  * multiplied, so the cost grows with window_tokens + sink_tokens and not with Skv.
  * Other arguments, layouts, statistics, limits and errors are those of attn_fwd; Sq, Skv <= 2^30
  * (ATTN_ERR_UNSUPPORTED beyond).
- * Probabilities go to their product with V as one number of `dtype`, as in attn_fwd: to 2^-8 of themselves for
- * ATTN_BF16; for ATTN_F16 to 2^-11, and to no less than 2^-32 of the largest.
+ * In 16 bits probabilities go to their product with V as one number of `dtype`, as in attn_fwd: rounded by up to 2^-8
+ * of themselves for ATTN_BF16, for ATTN_F16 by 2^-11, or by 2^-32 of the row's largest where that is more (attn_fwd:
+ * 2^-25). Sums, statistics and the output's accumulation are float32.
  * NaN or infinite values in keys that a row does not see do not reach the row. In values of its own
  * sequence that it does not see they may (0 * NaN), where a key tile (128 keys; 32 for ATTN_F32) holds
  * them beside keys that rows of its block see; those of other sequences never do.

@@ -400,6 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // are short of issue slots, not of the MUFU unit: 74 -> 70 us for 16 heads of 64), with sinks fewer, as the
   // polynomial is longer (one pair in 8 instead of 5: 181 -> 180 us for the packed case).
   constexpr int kEmu = kOwnP ? 0 : EXT == 3 ? 8 : kEmuEvery;
+  // P is one 16-bit number a weight, as in attn_fwd (2^-8 of it in bf16, 2^-11 in fp16; outputs of the packed case are
+  // off by 2.0e-3 instead of 1.6e-3 for it): a second term would add half of the products and another packing of every
+  // row to a kernel that waits for its softmax warps.
   // attn_fwd_sinks, fp16: P is kept times up to 2^7, relative to m = max - 7, as fp16 has fewer bits below 2^-14 and
   // none below 2^-25: many small weights behind one large one (a sink) count. With the 2^8 that the maximum may lag
   // behind, P stays within 2^15. Scores of 2^20 and more, whose own rounding is no longer small, go without.

@@ -14,7 +14,7 @@
 //
 // The tiles come by asynchronous copies, the next one while the current one is multiplied: with plain
 // loads a block of few key tiles spent most of its time waiting for them (2 x 4 x 333 x 80, window 128:
-// 121 us, now 22). Where rows are whole 16-byte chunks a row is one bulk copy, issued by four lanes of
+// 121 us, now 23). Where rows are whole 16-byte chunks a row is one bulk copy, issued by four lanes of
 // each warp: per-thread copies took every warp 2,000 of a tile's 7,000 cycles to issue (28 us; all rows
 // from one warp: 33), the queries with the first tile (25 -> 22 us). Rows are padded to whole 16-byte chunks, so that
 // queries and keys are read four columns at a time, and the weights four rows at a time: the loop is
