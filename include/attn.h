@@ -389,6 +389,7 @@ ATTN_API int attn_fwd_sinks(const void* q, const void* k, const void* v,
  * tensor cores (products exact, sums in float32, probabilities kept to 2^-16 of themselves; those of
  * ATTN_F16 also to no less than 2^-40 of the largest); other head
  * sizes up to 256, alignments and ATTN_F32 on the CUDA cores in float32. Nq / Nkv may be any integer.
+ * An infinite value at a visible position makes its column infinite or NaN.
  * workspace  device memory of attn_decode_workspace_size bytes, 16-byte aligned, filled with zeros
  *            once before its first use; every call leaves it ready for the next one, of any sizes that
  *            it is large enough for. Calls that may overlap on the device (other streams, graphs
